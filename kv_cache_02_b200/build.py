@@ -32,7 +32,7 @@ NVCC_FLAGS = [
 
 
 def sources() -> list:
-    return sorted(glob.glob(os.path.join(HERE, "csrc", "*")) + [os.path.join(ROOT, "include", "gqa.h")])
+    return sorted(glob.glob(os.path.join(HERE, "csrc", "*")) + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
 def nvcc() -> str:

@@ -1,0 +1,573 @@
+// gqa_decode_mxfp4: the decode of decode.cuh over the 4-bit cache of mxfp4.cuh.
+//
+// Same work items, ring and split merge. A stage holds 128 keys: K and V
+// codes (64-byte rows, 64-byte swizzle), their scales (a 32-bit word per key
+// and tensor) and, with an item's first tile, its q rows. Each of the four
+// consumer warps takes 32 keys, as two independent 16-key blocks.
+//
+// Codes become fp16 by the hardware's e2m1 conversion, two at a time, and go
+// into fp16 MMAs with fp32 sums; the scales stay out of the products:
+//   S = sum over 32-dim blocks of 2^(E_k - 127) (q . code): an ldmatrix gives
+//     a lane 8 codes of one block of its key, so two 16-dim MMAs cover a block
+//     (q in the same order of dims), and their sum is scaled in fp32. q is
+//     held in fp16 over a power of two of its own per head, 2^8 at the top:
+//     exact for elements down to 2^-25 of the head's largest.
+//   O = sum over keys of P (V codes) 2^(E_v - 127): the scale goes with P.
+//     A transposing ldmatrix gives a lane 4 dims of two keys; byte permutes
+//     pair the keys.
+//
+// P 2^(E_v - 127) leaves fp16's range, so each warp holds a reference exponent
+// R per block and multiplies 2^14 P by 2^(E_v - R + 1). While every E_v of the
+// step lies in [R - 15, R] (E_v = R - j costs j bits of the range) that product
+// holds P's 11 bits down to P = 2^(j - 29) and anything of it down to
+// 2^(j - 39). A step outside the range raises R, or when the range itself is
+// too small takes the same product in bf16, whose exponents need no reference
+// (slower: a further conversion per code).
+#pragma once
+
+#include "decode.cuh"
+#include "mxfp4.cuh"
+
+namespace gqa {
+
+constexpr int kMxTileKeys = 128;
+constexpr int kMxWarpKeys = 32;
+constexpr int kMxStages = 3;
+constexpr int kMxCtasPerSm = 3;
+constexpr int kMxSpan = 15;      // E_v of the fp16 product: [R - kMxSpan, R]
+constexpr int kMxHeadroom = 2;   // a raised R lies this far above the step's largest E_v
+
+struct MxCfg {
+  static constexpr int kCodeBytes = kMxTileKeys * kMxRowBytes;
+  static constexpr int kScaleOff = 2 * kCodeBytes;                  // K scales, then V scales
+  static constexpr int kQOff = kScaleOff + 2 * kMxTileKeys * 4;
+  static constexpr int kStageBytes = kQOff + kDecHeadsPerCta * kMxD * 2;
+  static constexpr int kMergeFloats = kDecConsumerWarps * (2 * kDecHeadsPerCta + kDecHeadsPerCta * kMxD);
+  static constexpr int kMergeOff = kMxStages * kStageBytes;
+  static constexpr int kInfoOff = kMergeOff + kMergeFloats * 4;
+  static constexpr int kBarOff = kInfoOff + kMxStages * 16;
+  static constexpr int kSmemBytes = kBarOff + 2 * kMxStages * 8;
+};
+static_assert(MxCfg::kStageBytes % 1024 == 0, "stages start on the swizzle pattern");
+
+struct MxParams {
+  const uint8_t *k_scales, *v_scales;
+};
+
+// Byte offset of 16-byte chunk `chunk` (0..3) of row `row` of 64-byte rows
+// written by TMA with CU_TENSOR_MAP_SWIZZLE_64B.
+__device__ __forceinline__ uint32_t sw64(uint32_t row, uint32_t chunk) {
+  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+}
+
+// 8 codes of a word -> 4 f16x2: r[i] = (code 2 i, code 2 i + 1)
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
+// Four scale bytes -> their values 2^(E - 127) (NaN for 255), by way of bf16, which holds every one of them.
+__device__ __forceinline__ void e8m0x4_to_f32(uint32_t w, float (&s)[4]) {
+  uint32_t lo, hi;
+  asm("{\n .reg .b16 h0, h1;\n mov.b32 {h0, h1}, %2;\n"
+      " cvt.rn.bf16x2.ue8m0x2 %0, h0;\n cvt.rn.bf16x2.ue8m0x2 %1, h1;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  s[0] = __uint_as_float(lo << 16);
+  s[1] = __uint_as_float(lo & 0xffff0000u);
+  s[2] = __uint_as_float(hi << 16);
+  s[3] = __uint_as_float(hi & 0xffff0000u);
+}
+
+// D(16x8) = A(16x16) * B(16x8), fp16 operands
+__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                   uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
+// f16x2 -> bf16x2; the e2m1 values are exact in both
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_bf16x2(f.x, f.y);
+}
+
+// Running state of one consumer warp. l is held times 2^14, o times 2^15 and
+// over 2^(R - 127) of its 32-dim block; m is the running maximum of the scores.
+struct MxState {
+  float m_a, m_b, l_a, l_b;
+  uint32_t ref;  // R of block i in byte i, 16 or more; the same in all lanes
+  float o[kMxD / 16][4];
+  __device__ __forceinline__ void reset() {
+    m_a = m_b = -INFINITY;
+    l_a = l_b = 0.f;
+    ref = 0x10101010u;
+#pragma unroll
+    for (int i = 0; i < kMxD / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  }
+};
+
+// Q^T as the fp16 B operand: in the MMA ks = 2 b + s the lane holds head
+// lane / 4, dims 32 b + 8 (lane % 4) + 4 s + {0, 1} and + {2, 3}. Returns the
+// power of two that the head's elements were divided by.
+__device__ __forceinline__ float load_q_frag_mx(uint32_t (&qf)[kMxD / 16][2], const __nv_bfloat16* q, int lane,
+                                                int nh) {
+  const int hn = lane >> 2;
+  const bool hv = hn < nh;
+  const uint4* row = reinterpret_cast<const uint4*>(q + (size_t)(hv ? hn : 0) * kMxD);
+  uint32_t u[4][4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint4 w = row[b * 4 + (lane & 3)];
+    u[b][0] = w.x, u[b][1] = w.y, u[b][2] = w.z, u[b][3] = w.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max((u[b][i] << 16) & 0x7fff0000u, u[b][i] & 0x7fff0000u));
+  }
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // 2^8 / 2^floor(log2 top): exponent fields 27 .. 253 keep both powers in range
+  const uint32_t e = min(max(top >> 23, 27u), 246u);
+  const float down = __uint_as_float((262u - e) << 23), up = __uint_as_float((e - 8u) << 23);
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(u[b][i] << 16) * down, hi = __uint_as_float(u[b][i] & 0xffff0000u) * down;
+      qf[2 * b + (i >> 1)][i & 1] = hv ? pack_f16x2(lo, hi) : 0u;
+    }
+  return up;
+}
+
+// The step's V scales do not lie within every block's [R - 15, R] (in some
+// lane): raise the references that have to be. True if all lie within then.
+__device__ __forceinline__ bool mx_rebase(MxState& st, uint32_t own, bool valid) {
+  uint32_t ref = 0;
+  bool fits = true;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t e = (own >> (8 * b)) & 255u;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, valid && e != 255u ? e : 0u);
+    const uint32_t old = (st.ref >> (8 * b)) & 255u;
+    uint32_t r = old;
+    if (top > old) {
+      r = min(254u, top + kMxHeadroom);
+      const float f = r - old > 126u ? 0.f : __uint_as_float((127u - (r - old)) << 23);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st.o[2 * b + i][j] *= f;
+    }
+    fits = fits && (!valid || (e <= r && r - e <= (uint32_t)kMxSpan));
+    ref |= r << (8 * b);
+  }
+  st.ref = ref;
+  return __all_sync(0xffffffffu, fits);
+}
+
+// 2^(E - R + 1) as bf16 bits; E <= R or 255 (NaN)
+__device__ __forceinline__ uint32_t mx_bf16_scale(uint32_t e, uint32_t r) {
+  return e == 255u ? 0x7fc0u : r - e > 126u ? 0u : (128u - (r - e)) << 7;
+}
+
+// One warp's 32 keys (kb .. kb + 31) of the tile in `stage`; `rows` keys of
+// the tile are valid, kb < rows. f_a, f_b: scale * log2(e) * the power of two
+// of the lane's heads.
+__device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[kMxD / 16][2], float f_a, float f_b,
+                                             const uint8_t* stage, int kb, int rows, int lane) {
+  using C = MxCfg;
+  const uint32_t k_base = smem_u32(stage);
+  const uint32_t v_base = k_base + C::kCodeBytes;
+  const uint32_t* sk = reinterpret_cast<const uint32_t*>(stage + C::kScaleOff);
+  const uint32_t* sv = sk + kMxTileKeys;
+  // ldmatrix: (rows 0-7, chunk c) (rows 8-15, chunk c) (rows 0-7, chunk c + 1) (rows 8-15, chunk c + 1)
+  const int row = kb + (lane & 7) + ((lane >> 3) & 1) * 8;
+  const int ch = lane >> 4;
+
+  // scores: key kb + lane / 4 + 8 i, i < 4
+  const int key0 = kb + (lane >> 2);
+  float xa[4], xb[4];
+#pragma unroll
+  for (int nb = 0; nb < 2; ++nb) {
+    float s0[4], s1[4];
+    e8m0x4_to_f32(sk[key0 + 16 * nb], s0);
+    e8m0x4_to_f32(sk[key0 + 16 * nb + 8], s1);
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t r[4];
+      ldmatrix_x4(k_base + sw64(row + 16 * nb, 2 * j + ch), r[0], r[1], r[2], r[3]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int b = 2 * j + i;
+        uint32_t lo[4], hi[4];
+        e2m1x8_to_f16(r[2 * i], lo);
+        e2m1x8_to_f16(r[2 * i + 1], hi);
+        float c[4];
+        mma_f16_16816_zero(c, lo[0], hi[0], lo[1], hi[1], qf[2 * b][0], qf[2 * b][1]);
+        mma_f16_16816(c, lo[2], hi[2], lo[3], hi[3], qf[2 * b + 1][0], qf[2 * b + 1][1]);
+        t[0] = fmaf(c[0], s0[b], t[0]);
+        t[1] = fmaf(c[1], s0[b], t[1]);
+        t[2] = fmaf(c[2], s1[b], t[2]);
+        t[3] = fmaf(c[3], s1[b], t[3]);
+      }
+    }
+    xa[2 * nb] = t[0] * f_a;
+    xb[2 * nb] = t[1] * f_b;
+    xa[2 * nb + 1] = t[2] * f_a;
+    xb[2 * nb + 1] = t[3] * f_b;
+  }
+  const bool partial = kb + kMxWarpKeys > rows;
+  if (partial) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (key0 + 8 * i >= rows) xa[i] = xb[i] = -INFINITY;
+  }
+
+  float mx_a = fmaxf(fmaxf(xa[0], xa[1]), fmaxf(xa[2], xa[3]));
+  float mx_b = fmaxf(fmaxf(xb[0], xb[1]), fmaxf(xb[2], xb[3]));
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
+    mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
+  }
+  const float mn_a = fmaxf(st.m_a, mx_a), mn_b = fmaxf(st.m_b, mx_b);
+  if (__any_sync(0xffffffffu, mn_a != st.m_a || mn_b != st.m_b)) {
+    const float al_a = fast_exp2(st.m_a - mn_a), al_b = fast_exp2(st.m_b - mn_b);
+    st.m_a = mn_a;
+    st.m_b = mn_b;
+    st.l_a *= al_a;
+    st.l_b *= al_b;
+#pragma unroll
+    for (int md = 0; md < kMxD / 16; ++md) {
+      st.o[md][0] *= al_a;
+      st.o[md][1] *= al_b;
+      st.o[md][2] *= al_a;
+      st.o[md][3] *= al_b;
+    }
+  }
+  float pa[4], pb[4];
+  const float r_a = mn_a - 14.f, r_b = mn_b - 14.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    pa[i] = fast_exp2(xa[i] - r_a);
+    pb[i] = fast_exp2(xb[i] - r_b);
+  }
+  st.l_a += (pa[0] + pa[1]) + (pa[2] + pa[3]);
+  st.l_b += (pb[0] + pb[1]) + (pb[2] + pb[3]);
+
+  // V scales: the keys 2 (lane % 4) + {0, 1} + 8 i of the P^T operand; those past the valid rows: 2^0 times P = 0
+  uint2 ev[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ev[i] = *reinterpret_cast<const uint2*>(sv + kb + 2 * (lane & 3) + 8 * i);
+  const uint32_t own = sv[kb + lane];
+  const bool own_valid = kb + lane < rows;
+  // R - E of each byte in 0 .. 15: the bytes in two halves with a guard bit above each
+  const uint32_t d0 = ((st.ref & 0x00ff00ffu) | 0x01000100u) - (own & 0x00ff00ffu);
+  const uint32_t d1 = (((st.ref >> 8) & 0x00ff00ffu) | 0x01000100u) - ((own >> 8) & 0x00ff00ffu);
+  const bool fits = (((d0 & 0x01f001f0u) ^ 0x01000100u) | ((d1 & 0x01f001f0u) ^ 0x01000100u)) == 0u;
+  bool fast = __all_sync(0xffffffffu, fits || !own_valid);
+  if (!fast) fast = mx_rebase(st, own, own_valid);
+  const uint32_t ref = st.ref;
+  if (partial) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = kb + 2 * (lane & 3) + 8 * i;
+      if (k >= rows) ev[i].x = ref;
+      if (k + 1 >= rows) ev[i].y = ref;
+    }
+  }
+
+  if (fast) {
+    // f16 exponent fields E - R + 16 (1 .. 16 in each byte), moved to where they sit in a half's high byte
+    const uint32_t base4 = (ref - 0x10101010u) << 2;
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) {
+      uint32_t pt[2], e0[2], e1[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        pt[i] = movmatrix_trans(pack_f16x2(pa[2 * nb + i], pb[2 * nb + i]));
+        e0[i] = ev[2 * nb + i].x * 4u - base4;
+        e1[i] = ev[2 * nb + i].y * 4u - base4;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t r[4];
+        ldmatrix_x4_trans(v_base + sw64(row + 16 * nb, 2 * j + ch), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int b = 2 * j + i;
+          constexpr uint32_t kSel[4] = {0x4000u, 0x5010u, 0x6020u, 0x7030u};
+          const uint32_t q0 = hmul2(pt[0], __byte_perm(e0[0], e1[0], kSel[b]) & 0xff00ff00u);
+          const uint32_t q1 = hmul2(pt[1], __byte_perm(e0[1], e1[1], kSel[b]) & 0xff00ff00u);
+          uint32_t lo[4], hi[4];  // keys 2t, 2t + 1: (k0 d0 d1) (k0 d2 d3) (k1 d0 d1) (k1 d2 d3)
+          e2m1x8_to_f16(r[2 * i], lo);
+          e2m1x8_to_f16(r[2 * i + 1], hi);
+          mma_f16_16816(st.o[2 * b], __byte_perm(lo[0], lo[2], 0x5410), __byte_perm(lo[0], lo[2], 0x7632),
+                        __byte_perm(hi[0], hi[2], 0x5410), __byte_perm(hi[0], hi[2], 0x7632), q0, q1);
+          mma_f16_16816(st.o[2 * b + 1], __byte_perm(lo[1], lo[3], 0x5410), __byte_perm(lo[1], lo[3], 0x7632),
+                        __byte_perm(hi[1], hi[3], 0x5410), __byte_perm(hi[1], hi[3], 0x7632), q0, q1);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) {
+      uint32_t pt[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) pt[i] = movmatrix_trans(pack_bf16x2(pa[2 * nb + i], pb[2 * nb + i]));
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j) {
+        uint32_t r[4];
+        ldmatrix_x4_trans(v_base + sw64(row + 16 * nb, 2 * j + ch), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int sh = 8 * (2 * j + i);
+          const uint32_t rb = (ref >> sh) & 255u;
+          uint32_t q[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint2 e = ev[2 * nb + u];
+            q[u] = bmul2(pt[u], mx_bf16_scale((e.x >> sh) & 255u, rb) | (mx_bf16_scale((e.y >> sh) & 255u, rb) << 16));
+          }
+          uint32_t lo[4], hi[4];
+          e2m1x8_to_f16(r[2 * i], lo);
+          e2m1x8_to_f16(r[2 * i + 1], hi);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            lo[u] = f16x2_to_bf16x2(lo[u]);
+            hi[u] = f16x2_to_bf16x2(hi[u]);
+          }
+          float acc[2][4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            acc[0][u] = j == 0 ? st.o[2 * i][u] : st.o[4 + 2 * i][u];
+            acc[1][u] = j == 0 ? st.o[2 * i + 1][u] : st.o[5 + 2 * i][u];
+          }
+          mma_bf16_16816(acc[0], __byte_perm(lo[0], lo[2], 0x5410), __byte_perm(lo[0], lo[2], 0x7632),
+                         __byte_perm(hi[0], hi[2], 0x5410), __byte_perm(hi[0], hi[2], 0x7632), q[0], q[1]);
+          mma_bf16_16816(acc[1], __byte_perm(lo[1], lo[3], 0x5410), __byte_perm(lo[1], lo[3], 0x7632),
+                         __byte_perm(hi[1], hi[3], 0x5410), __byte_perm(hi[1], hi[3], 0x7632), q[0], q[1]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (j == 0) {
+              st.o[2 * i][u] = acc[0][u];
+              st.o[2 * i + 1][u] = acc[1][u];
+            } else {
+              st.o[4 + 2 * i][u] = acc[0][u];
+              st.o[5 + 2 * i][u] = acc[1][u];
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+// End of a work item: the four warps' states merged, then the output (the
+// unit's only split) or the split's partial.
+__device__ __forceinline__ void mx_epilogue(const DecodeParams& p, const ItemCoord& c, const MxState& st, float* merge,
+                                            bool single, int tid, int warp, int lane) {
+  constexpr int D = kMxD;
+  float* red_m = merge;
+  float* red_l = red_m + kDecConsumerWarps * kDecHeadsPerCta;
+  float* ow = red_l + kDecConsumerWarps * kDecHeadsPerCta + warp * kDecHeadsPerCta * D;
+  consumer_bar();  // the previous item's scratch has been read
+  float l_a = st.l_a, l_b = st.l_b;
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    l_a += __shfl_xor_sync(0xffffffffu, l_a, off);
+    l_b += __shfl_xor_sync(0xffffffffu, l_b, off);
+  }
+  const int ha = 2 * (lane & 3);
+  if (lane < 4) {
+    red_m[warp * 8 + ha] = st.m_a;
+    red_m[warp * 8 + ha + 1] = st.m_b;
+    red_l[warp * 8 + ha] = l_a;
+    red_l[warp * 8 + ha + 1] = l_b;
+  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float f = __uint_as_float((((st.ref >> (8 * b)) & 255u) - 1u) << 23);  // 2^(R - 127) / 2
+    const int dim = 32 * b + 4 * (lane >> 2);
+    const float* o0 = st.o[2 * b];
+    const float* o1 = st.o[2 * b + 1];
+    *reinterpret_cast<float4*>(ow + ha * D + dim) = make_float4(o0[0] * f, o0[2] * f, o1[0] * f, o1[2] * f);
+    *reinterpret_cast<float4*>(ow + (ha + 1) * D + dim) = make_float4(o0[1] * f, o0[3] * f, o1[1] * f, o1[3] * f);
+  }
+  consumer_bar();
+  __nv_bfloat16* out_row = static_cast<__nv_bfloat16*>(p.out) + ((size_t)c.b * p.H + c.h0) * D;
+  const size_t part = ((size_t)c.unit * p.nsplit + c.split) * p.G + (size_t)c.hsl * kDecHeadsPerCta;
+  for (int i = tid; i < c.nh * D; i += kDecConsumerWarps * 32) {
+    const int h = i / D, dim = i % D;
+    float M, L, O;
+    merged<D>(merge, h, dim, M, L, O);
+    if (single) {
+      out_row[i] = __float2bfloat16_rn(O / L);
+    } else {
+      p.ws_o[(part + h) * D + dim] = O;
+      if (dim == 0) p.ws_ml[part + h] = make_float2(M, L);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kDecThreads, kMxCtasPerSm)
+    decode_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
+                        const DecodeParams p, const MxParams mp) {
+  using C = MxCfg;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* merge = reinterpret_cast<float*>(smem + C::kMergeOff);
+  StageInfo* info = reinterpret_cast<StageInfo*>(smem + C::kInfoOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + kMxStages;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (smem_u32(smem) & 1023u) {  // the swizzle pattern needs aligned stages
+    grid_dep_wait();
+    if (threadIdx.x == 0) raise_error(GQA_DEVERR_TIMEOUT);
+    return;
+  }
+  // before the grid dependency, as in decode_bf16_kernel: barriers, descriptors, an L2 warm-up (a hint) of the
+  // first work item's codes, sized by a length that may be stale
+  int spec_first = 0;
+  if (warp == kDecConsumerWarps && lane == 0) {
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+    prefetch_tensormap(&tm_k16);
+    prefetch_tensormap(&tm_v16);
+    if ((int)blockIdx.x < p.nitems) spec_first = __ldcg(p.seqlens + item_coord(p, blockIdx.x).b);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMxStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kDecConsumerWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (warp == kDecConsumerWarps && lane == 0 && (int)blockIdx.x < p.nitems)
+    warm_first_item<kMxRowBytes>(p, item_coord(p, blockIdx.x), spec_first, kMxStages * kMxTileKeys);
+  grid_dep_wait();
+  grid_dep_launch();
+
+  if (warp == kDecConsumerWarps) {
+    if (lane != 0) return;
+    const uint64_t policy = l2_policy_evict_first();
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+    int it = 0;
+    bool ok = true;
+    for (int k = 0;; ++k) {
+      const int ticket = k == 0 ? 1 : take_ticket(p.ws_queue, p.tag);
+      const int item = k == 0 ? (int)blockIdx.x : (int)gridDim.x + ticket - 1;
+      if (ticket <= 0 || item >= p.nitems) break;
+      const ItemCoord c = item_coord(p, item);
+      const int raw = __ldg(p.seqlens + c.b);
+      const int len = valid_len(raw, p.S_max);
+      if (c.g == 0 && c.split == 0 && c.hsl == 0 && len != raw) raise_error(GQA_DEVERR_SEQLEN);
+      const int t_begin = c.split * p.chunk;
+      const int t_end = min(len, t_begin + p.chunk);
+      if (t_begin >= t_end) {
+        if (c.split == 0) {  // an empty sequence: zeros for this item's heads
+          uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)c.b * p.H + c.h0) * kMxD);
+          for (int i = 0; i < c.nh * kMxD / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      const int ntiles = (t_end - t_begin + kMxTileKeys - 1) / kMxTileKeys;
+      for (int tt = 0; tt < ntiles; ++tt, ++it) {
+        const int s = it % kMxStages;
+        const int t0 = t_begin + tt * kMxTileKeys;
+        const int rows = min(kMxTileKeys, t_end - t0);
+        if (it >= kMxStages) ok = mbar_wait_bounded(&empty[s], ((it / kMxStages) - 1) & 1);
+        if (!ok) break;
+        info[s] = StageInfo{item, rows,
+                            (tt == 0 ? kTileFirst : 0) | (tt == ntiles - 1 ? kTileLast : 0) |
+                                (len <= p.chunk ? kUnitSingleSplit : 0),
+                            -1};
+        uint8_t* stage = smem + s * C::kStageBytes;
+        const uint32_t sbytes = (uint32_t)((rows + 3) / 4 * 16);  // S_max is a multiple of 4: within the unit's scales
+        const uint32_t q_bytes = tt == 0 ? (uint32_t)(c.nh * kMxD * 2) : 0u;
+        const int row0 = c.unit * p.S_max + t0;
+        if (rows == kMxTileKeys) {
+          mbar_arrive_expect_tx(&full[s], 2u * C::kCodeBytes + 2u * sbytes + q_bytes);
+          tma_load_2d(stage, &tm_k, 0, row0, &full[s], policy);
+          tma_load_2d(stage + C::kCodeBytes, &tm_v, 0, row0, &full[s], policy);
+        } else {
+          const int nbox = (rows + kDecBoxRows - 1) / kDecBoxRows;
+          mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * nbox * kDecBoxRows * kMxRowBytes) + 2u * sbytes + q_bytes);
+          for (int bx = 0; bx < nbox; ++bx) {
+            const int off = bx * kDecBoxRows * kMxRowBytes;
+            tma_load_2d(stage + off, &tm_k16, 0, row0 + bx * kDecBoxRows, &full[s], policy);
+            tma_load_2d(stage + C::kCodeBytes + off, &tm_v16, 0, row0 + bx * kDecBoxRows, &full[s], policy);
+          }
+        }
+        bulk_load(stage + C::kScaleOff, mp.k_scales + (size_t)row0 * kMxScales, sbytes, &full[s]);
+        bulk_load(stage + C::kScaleOff + kMxTileKeys * 4, mp.v_scales + (size_t)row0 * kMxScales, sbytes, &full[s]);
+        if (q_bytes)
+          bulk_load(stage + C::kQOff, static_cast<const __nv_bfloat16*>(p.q) + ((size_t)c.b * p.H + c.h0) * kMxD,
+                    q_bytes, &full[s]);
+      }
+      if (!ok) break;
+    }
+    leave_queue(p.ws_queue, p.tag);
+    if (ok) {  // a record without loads ends the consumers' loop
+      const int s = it % kMxStages;
+      if (it >= kMxStages) ok = mbar_wait_bounded(&empty[s], ((it / kMxStages) - 1) & 1);
+      if (ok) {
+        info[s] = StageInfo{-1, 0, 0, 0};
+        mbar_arrive(&full[s]);
+        ++it;
+      }
+    }
+    // this CTA's own loads must land before the block may exit
+    for (int j = max(0, it - kMxStages); j < it; ++j) mbar_wait_bounded(&full[j % kMxStages], (j / kMxStages) & 1);
+    return;
+  }
+
+  const int tid = threadIdx.x;
+  const int kb = warp * kMxWarpKeys;
+  uint32_t qf[kMxD / 16][2];
+  float f_a = 0.f, f_b = 0.f;
+  MxState st;
+  ItemCoord cur{};
+  for (int it = 0;; ++it) {
+    const int s = it % kMxStages;
+    if (!mbar_wait_bounded(&full[s], (it / kMxStages) & 1)) break;
+    const StageInfo si = info[s];
+    if (si.item < 0) break;
+    const uint8_t* stage = smem + s * C::kStageBytes;
+    if (si.flags & kTileFirst) {
+      cur = item_coord(p, si.item);
+      const float up =
+          load_q_frag_mx(qf, reinterpret_cast<const __nv_bfloat16*>(stage + C::kQOff), lane, cur.nh) * p.scale_log2;
+      f_a = __shfl_sync(0xffffffffu, up, 8 * (lane & 3));
+      f_b = __shfl_sync(0xffffffffu, up, 8 * (lane & 3) + 4);
+      st.reset();
+    }
+    if (kb < si.rows) warp_tile_mx(st, qf, f_a, f_b, stage, kb, si.rows, lane);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    if (si.flags & kTileLast) mx_epilogue(p, cur, st, merge, (si.flags & kUnitSingleSplit) != 0, tid, warp, lane);
+  }
+}
+
+}  // namespace gqa

@@ -1,0 +1,326 @@
+// gqa_decode_scores: the decode of decode.cuh, and each cached row's share of
+// the attention added to its score.
+//
+//   scores[b, g, t] += sum_{h in group} 2^(x[h, t] - M[h]) / L[h]
+//
+// with x the scaled scores in log2 units and (M, L) the softmax's maximum and
+// sum over all of the sequence's keys. A row's weight is not known before the
+// last split's maximum is, so the decode kernel stores its scaled scores
+// (float32: a weight is as exact as its exponent) and a second kernel turns
+// them into weights once (M, L) of every split are there. Reading K again
+// instead would cost 2 d bytes a key; the scores are 8 G bytes a key written
+// and read back, mostly in L2.
+#pragma once
+
+#include "decode.cuh"
+
+namespace gqa {
+
+struct ScoresParams {
+  float* x;       // [B * K, S_max, gp] scaled scores of the group's heads
+  float* scores;  // [B, K, S_max]
+  int gp;         // G rounded up to even: a lane stores two heads at a time
+};
+
+// warp_tile of decode.cuh, storing the scaled scores of the warp's keys at
+// xrow (the row of key kb in x, at the lane's first head; null: no such head).
+template <int D>
+__device__ __forceinline__ void warp_tile_scores(WarpState<D>& st, const uint32_t (&qf)[D / 16][2],
+                                                 uint32_t stage_addr, int kb, int rows, int lane, float scale_log2,
+                                                 float* xrow, int gp) {
+  using C = DecCfg<D>;
+  const uint32_t k_base = stage_addr;
+  const uint32_t v_base = stage_addr + C::kTileBytes;
+  const int k_row = kb + (lane & 7) + ((lane >> 3) & 1) * 8;
+  const int k_col8 = lane >> 4;
+  const int v_row = kb + (lane & 7) + (lane >> 4) * 8;
+  const int v_col8 = (lane >> 3) & 1;
+
+  float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const int chunk = ks * 2 + k_col8;
+    const uint32_t addr = k_base + (chunk >> 3) * C::kHalfBytes + sw128(k_row, chunk & 7);
+    uint32_t a0, a1, a2, a3;
+    ldmatrix_x4(addr, a0, a1, a2, a3);
+    mma_bf16_16816(c, a0, a1, a2, a3, qf[ks][0], qf[ks][1]);
+  }
+
+  const int key0 = kb + (lane >> 2);
+  const bool v0 = key0 < rows, v1 = key0 + 8 < rows;
+  const float x0 = v0 ? c[0] * scale_log2 : -INFINITY;
+  const float x1 = v0 ? c[1] * scale_log2 : -INFINITY;
+  const float x2 = v1 ? c[2] * scale_log2 : -INFINITY;
+  const float x3 = v1 ? c[3] * scale_log2 : -INFINITY;
+  if (xrow != nullptr) {
+    float* dst = xrow + (lane >> 2) * gp;
+    if (v0) *reinterpret_cast<float2*>(dst) = make_float2(x0, x1);
+    if (v1) *reinterpret_cast<float2*>(dst + 8 * gp) = make_float2(x2, x3);
+  }
+  float mx_a = fmaxf(x0, x2), mx_b = fmaxf(x1, x3);
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
+    mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
+  }
+  const float mn_a = fmaxf(st.m_a, mx_a), mn_b = fmaxf(st.m_b, mx_b);
+  const float al_a = fast_exp2(st.m_a - mn_a), al_b = fast_exp2(st.m_b - mn_b);
+  st.m_a = mn_a;
+  st.m_b = mn_b;
+  const float p0 = fast_exp2(x0 - mn_a), p1 = fast_exp2(x1 - mn_b);
+  const float p2 = fast_exp2(x2 - mn_a), p3 = fast_exp2(x3 - mn_b);
+  st.l_a = st.l_a * al_a + p0 + p2;
+  st.l_b = st.l_b * al_b + p1 + p3;
+#pragma unroll
+  for (int md = 0; md < D / 16; ++md) {
+    st.o[md][0] *= al_a;
+    st.o[md][1] *= al_b;
+    st.o[md][2] *= al_a;
+    st.o[md][3] *= al_b;
+  }
+
+  const uint32_t pb0 = movmatrix_trans(pack_bf16x2(p0, p1));
+  const uint32_t pb1 = movmatrix_trans(pack_bf16x2(p2, p3));
+  uint32_t mask_lo = 0xffffffffu, mask_hi = 0xffffffffu;
+  if (kb + 16 > rows) {
+    const int lim = rows - kb;
+    const int kk = 2 * (lane & 3);
+    mask_lo = (kk < lim ? 0x0000ffffu : 0u) | (kk + 1 < lim ? 0xffff0000u : 0u);
+    mask_hi = (kk + 8 < lim ? 0x0000ffffu : 0u) | (kk + 9 < lim ? 0xffff0000u : 0u);
+  }
+#pragma unroll
+  for (int md = 0; md < D / 16; ++md) {
+    const int chunk = md * 2 + v_col8;
+    const uint32_t addr = v_base + (chunk >> 3) * C::kHalfBytes + sw128(v_row, chunk & 7);
+    uint32_t a0, a1, a2, a3;
+    ldmatrix_x4_trans(addr, a0, a1, a2, a3);
+    mma_bf16_16816(st.o[md], a0 & mask_lo, a1 & mask_lo, a2 & mask_hi, a3 & mask_hi, pb0, pb1);
+  }
+}
+
+// End of a work item: as item_epilogue, and (m, l) of every split is kept,
+// the only split's too.
+template <int D>
+__device__ __forceinline__ void scores_epilogue(const DecodeParams& p, const ItemCoord& c, const WarpState<D>& st,
+                                                float* merge, bool single, int tid, int warp, int lane) {
+  __nv_bfloat16* out_row = static_cast<__nv_bfloat16*>(p.out) + ((size_t)c.b * p.H + c.h0) * D;
+  consumer_bar();
+  stash_warp_state<D>(merge, st, warp, lane);
+  consumer_bar();
+  const size_t part = ((size_t)c.unit * p.nsplit + c.split) * p.G + (size_t)c.hsl * kDecHeadsPerCta;
+  for (int i = tid; i < c.nh * D; i += kDecConsumerWarps * 32) {
+    const int h = i / D, dim = i % D;
+    float M, L, O;
+    merged<D>(merge, h, dim, M, L, O);
+    if (single)
+      out_row[i] = __float2bfloat16_rn(O / L);
+    else
+      p.ws_o[(part + h) * D + dim] = O;
+    if (dim == 0) p.ws_ml[part + h] = make_float2(M, L);
+  }
+}
+
+// Producer of a contiguous bf16 cache (one thread): work items from the
+// counter, their tiles through the ring, then a record that ends the
+// consumers' loop. As in decode_bf16_kernel.
+template <int D>
+__device__ __forceinline__ void produce_contiguous(const DecodeParams& p, uint8_t* smem, StageInfo* info,
+                                                   uint64_t* full, uint64_t* empty, const CUtensorMap* tm_k64,
+                                                   const CUtensorMap* tm_v64, const CUtensorMap* tm_k16,
+                                                   const CUtensorMap* tm_v16) {
+  using C = DecCfg<D>;
+  const uint64_t policy = l2_policy_evict_first();
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+  int it = 0;
+  bool ok = true;
+  for (int k = 0;; ++k) {
+    const int ticket = k == 0 ? 1 : take_ticket(p.ws_queue, p.tag);
+    const int item = k == 0 ? (int)blockIdx.x : (int)gridDim.x + ticket - 1;
+    if (ticket <= 0 || item >= p.nitems) break;
+    const ItemCoord c = item_coord(p, item);
+    const int raw = __ldg(p.seqlens + c.b);
+    const int len = valid_len(raw, p.S_max);
+    if (c.g == 0 && c.split == 0 && c.hsl == 0 && len != raw) raise_error(GQA_DEVERR_SEQLEN);
+    const int t_begin = c.split * p.chunk;
+    const int t_end = min(len, t_begin + p.chunk);
+    if (t_begin >= t_end) {
+      if (c.split == 0) {  // an empty sequence: zeros for this item's heads
+        uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)c.b * p.H + c.h0) * D);
+        for (int i = 0; i < c.nh * D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      continue;
+    }
+    const int ntiles = (t_end - t_begin + kDecTileKeys - 1) / kDecTileKeys;
+    for (int tt = 0; tt < ntiles && ok; ++tt, ++it) {
+      const int s = it % C::kStages;
+      const int t0 = t_begin + tt * kDecTileKeys;
+      const int rows = min(kDecTileKeys, t_end - t0);
+      if (it >= C::kStages) ok = mbar_wait_bounded(&empty[s], ((it / C::kStages) - 1) & 1);
+      if (!ok) break;
+      info[s] = StageInfo{item, rows,
+                          (tt == 0 ? kTileFirst : 0) | (tt == ntiles - 1 ? kTileLast : 0) |
+                              (len <= p.chunk ? kUnitSingleSplit : 0),
+                          -1};
+      issue_tile<D>(smem + s * C::kStageBytes, &full[s], tm_k64, tm_v64, tm_k16, tm_v16, c.unit * p.S_max + t0, rows,
+                    policy);
+    }
+    if (!ok) break;
+  }
+  leave_queue(p.ws_queue, p.tag);
+  if (ok) {
+    const int s = it % C::kStages;
+    if (it >= C::kStages) ok = mbar_wait_bounded(&empty[s], ((it / C::kStages) - 1) & 1);
+    if (ok) {
+      info[s] = StageInfo{-1, 0, 0, 0};
+      mbar_arrive(&full[s]);
+      ++it;
+    }
+  }
+  for (int j = max(0, it - C::kStages); j < it; ++j) mbar_wait_bounded(&full[j % C::kStages], (j / C::kStages) & 1);
+}
+
+template <int D, bool kPaged>
+__global__ void __launch_bounds__(kDecThreads, 2)
+    decode_scores_kernel(const __grid_constant__ CUtensorMap tm_k64, const __grid_constant__ CUtensorMap tm_v64,
+                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const DecodeParams p, const ScoresParams sp) {
+  using C = DecCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* merge = reinterpret_cast<float*>(smem + C::kMergeOff);
+  StageInfo* info = reinterpret_cast<StageInfo*>(smem + C::kInfoOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + C::kStages;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (smem_u32(smem) & 1023u) {  // the swizzle pattern needs 1024-byte aligned stages
+    grid_dep_wait();
+    if (threadIdx.x == 0) raise_error(GQA_DEVERR_TIMEOUT);
+    return;
+  }
+  // before the grid dependency: barriers, descriptors and an L2 warm-up of
+  // the first work item's rows, as in decode_bf16_kernel
+  int spec_first = 0;
+  if (!kPaged && warp == kDecConsumerWarps && lane == 0) {
+    prefetch_tensormap(&tm_k64);
+    prefetch_tensormap(&tm_v64);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+    if ((int)blockIdx.x < p.nitems) spec_first = __ldcg(p.seqlens + item_coord(p, blockIdx.x).b);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kDecConsumerWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (!kPaged && warp == kDecConsumerWarps && lane == 0 && (int)blockIdx.x < p.nitems)
+    warm_first_item<D * C::kElt>(p, item_coord(p, blockIdx.x), spec_first, kDecWarmKeys);
+  if (kPaged && warp == kDecConsumerWarps && (int)blockIdx.x < p.nitems) {
+    const ItemCoord c0 = item_coord(p, blockIdx.x);
+    warm_first_item_paged<D>(p, c0, __ldcg(p.seqlens + c0.b), kDecWarmKeys, lane);
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+
+  if (warp == kDecConsumerWarps) {
+    if constexpr (kPaged)
+      produce_paged<D>(p, smem, info, full, empty, &tm_k64, &tm_v64, &tm_k, &tm_v, lane);
+    else if (lane == 0)
+      produce_contiguous<D>(p, smem, info, full, empty, &tm_k64, &tm_v64, &tm_k, &tm_v);
+    return;
+  }
+
+  const int tid = threadIdx.x;
+  const int kb = warp * 16;
+  uint32_t qf[D / 16][2];
+  int t0 = 0;  // key of the tile's first row
+  WarpState<D> st;
+  ItemCoord cur{};
+  for (int it = 0;; ++it) {
+    const int s = it % C::kStages;
+    if (!mbar_wait_bounded(&full[s], (it / C::kStages) & 1)) break;
+    const StageInfo si = info[s];
+    if (si.item < 0) break;
+    if (si.flags & kTileFirst) {
+      cur = item_coord(p, si.item);
+      load_q_frag<D>(qf, static_cast<const __nv_bfloat16*>(p.q) + ((size_t)cur.b * p.H + cur.h0) * D, lane, cur.nh);
+      st.reset();
+      t0 = cur.split * p.chunk;
+    }
+    if (kb < si.rows) {
+      const int h = 2 * (lane & 3);
+      float* xrow = h < cur.nh ? sp.x + ((size_t)cur.unit * p.S_max + t0 + kb) * sp.gp + cur.hsl * kDecHeadsPerCta + h
+                               : nullptr;
+      warp_tile_scores<D>(st, qf, smem_u32(smem + s * C::kStageBytes), kb, si.rows, lane, p.scale_log2, xrow, sp.gp);
+    }
+    t0 += kDecTileKeys;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    if (si.flags & kTileLast)
+      scores_epilogue<D>(p, cur, st, merge, (si.flags & kUnitSingleSplit) != 0, tid, warp, lane);
+  }
+}
+
+// Scores += weights. A CTA takes kAccKeys rows of one unit: its warps first
+// join the splits' (m, l) of the group's heads, then a thread per row adds up
+// the heads' weights in order.
+constexpr int kAccThreads = 256;
+constexpr int kAccKeys = 1024;
+constexpr int kAccHeads = 64;  // heads whose (M, 1 / L) are held at a time
+
+__global__ void __launch_bounds__(kAccThreads)
+    scores_accumulate_kernel(const DecodeParams p, const ScoresParams sp, int chunks) {
+  __shared__ float2 ml[kAccHeads];
+  const int unit = blockIdx.x / chunks;
+  const int b = unit / p.K;
+  const int k0 = (blockIdx.x % chunks) * kAccKeys;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int len = valid_len(p.seqlens[b], p.S_max);
+  const int n = min(kAccKeys, len - k0);
+  if (n <= 0) return;
+  const int ns = (len + p.chunk - 1) / p.chunk;
+  float acc[kAccKeys / kAccThreads];
+#pragma unroll
+  for (int j = 0; j < kAccKeys / kAccThreads; ++j) acc[j] = 0.f;
+  for (int h0 = 0; h0 < p.G; h0 += kAccHeads) {
+    const int nh = min(kAccHeads, p.G - h0);
+    __syncthreads();
+    for (int h = warp; h < nh; h += kAccThreads / 32) {
+      const float2* part = p.ws_ml + (size_t)unit * p.nsplit * p.G + h0 + h;
+      float M = -INFINITY, L = 0.f;
+      for (int s = lane; s < ns; s += 32) M = fmaxf(M, __ldcg(&part[(size_t)s * p.G].x));
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      for (int s = lane; s < ns; s += 32) {
+        const float2 m = __ldcg(&part[(size_t)s * p.G]);
+        L += m.y * fast_exp2(m.x - M);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+      if (lane == 0) ml[h] = make_float2(M, 1.f / L);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kAccKeys / kAccThreads; ++j) {
+      const int i = tid + j * kAccThreads;
+      if (i >= n) continue;
+      const float2* x = reinterpret_cast<const float2*>(sp.x + ((size_t)unit * p.S_max + k0 + i) * sp.gp + h0);
+      for (int h = 0; h < nh; h += 2) {
+        const float2 v = __ldcg(x + h / 2);
+        acc[j] += fast_exp2(v.x - ml[h].x) * ml[h].y;
+        if (h + 1 < nh) acc[j] += fast_exp2(v.y - ml[h + 1].x) * ml[h + 1].y;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kAccKeys / kAccThreads; ++j) {
+    const int i = tid + j * kAccThreads;
+    if (i < n) sp.scores[(size_t)unit * p.S_max + k0 + i] += acc[j];
+  }
+}
+
+}  // namespace gqa

@@ -16,6 +16,7 @@
 #include <random>
 
 #include "../../include/gqa.h"
+#include "../../include/gqa_cache.h"
 #include "append_meanpool.cuh"
 #include "common.cuh"
 #include "decode.cuh"
@@ -23,6 +24,12 @@
 #include "prefill.cuh"
 #include "prefill_pair.cuh"
 #include "kv_proj.cuh"
+#include "norm_rope.cuh"
+#include "mxfp4.cuh"
+#include "decode_mxfp4.cuh"
+#include "decode_scores.cuh"
+#include "evict.cuh"
+#include "prompt_scores.cuh"
 
 namespace {
 
@@ -253,12 +260,13 @@ int wide_ctas_per_sm(int dev) {
   return n;
 }
 
-// int8: the 8-bit cache (narrow-group kernel only).
+// int8: the 8-bit cache (narrow-group kernel only); narrow: the narrow-group
+// kernels for every group size (gqa_decode_scores).
 DecodePlan plan_decode(int B, int H, int K, int S_max, int d, int num_splits, gqa_dtype dt, int sms,
-                       bool int8 = false, bool paged = false) {
+                       bool int8 = false, bool paged = false, bool narrow = false) {
   DecodePlan pl;
   const int G = H / K;
-  pl.wide = !int8 && dt == GQA_BF16 && d == 128 && G % gqa::kWideHeads == 0;
+  pl.wide = !int8 && !narrow && dt == GQA_BF16 && d == 128 && G % gqa::kWideHeads == 0;
   const int heads_per_cta =
       pl.wide ? gqa::kWideHeads : (dt == GQA_BF16 ? gqa::kDecHeadsPerCta : gqa::kDecF32HeadsPerCta);
   const int tile = pl.wide ? gqa::kWideKeys : 64;
@@ -931,3 +939,6 @@ int gqa_get_last_error(gqa_stream_t stream, uint32_t* bits) {
 }
 
 }  // extern "C"
+
+// the calls of include/gqa_cache.h
+#include "cache_lib.cuh"

@@ -1,4 +1,4 @@
-"""ctypes binding of libgqa.so (include/gqa.h), same names as the C ABI.
+"""ctypes binding of libgqa.so (include/gqa.h, include/gqa_cache.h), same names as the C ABI.
 
 Argument marshalling only: each function takes torch tensors that already
 live on the GPU, checks their shapes against one another, and passes raw
@@ -23,6 +23,7 @@ GQA_OK = 0
 GQA_ERR_DEVICE = -5
 GQA_ERR_UNSUPPORTED = -6
 GQA_DEVERR_APPEND_POS, GQA_DEVERR_SEQLEN, GQA_DEVERR_TIMEOUT, GQA_DEVERR_BLOCK = 0x1, 0x2, 0x4, 0x8
+GQA_DEVERR_ROPE_POS = 0x10
 
 GQA_ERR_SCRATCH_LIMIT = -7
 GQA_NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024
@@ -31,7 +32,12 @@ EXPORTED = ("gqa_kv_append", "gqa_decode_workspace_bytes", "gqa_decode", "gqa_de
             "gqa_decode_paged_workspace_bytes", "gqa_decode_paged", "gqa_decode_append_paged", "gqa_kv_append_paged",
             "gqa_decode_int8_workspace_bytes", "gqa_decode_int8", "gqa_kv_append_int8", "gqa_prefill_causal_varlen",
             "gqa_kv_project_workspace_bytes", "gqa_kv_project_append",
-            "gqa_prefill_causal", "gqa_meanpool_kv", "gqa_get_last_error", "gqa_status_string")
+            "gqa_prefill_causal", "gqa_meanpool_kv", "gqa_get_last_error", "gqa_status_string",
+            "gqa_rope_table", "gqa_qk_norm_rope", "gqa_qk_norm_rope_paged",
+            "gqa_decode_scores_workspace_bytes", "gqa_decode_scores", "gqa_decode_scores_paged_workspace_bytes",
+            "gqa_decode_scores_paged", "gqa_prompt_scores_workspace_bytes", "gqa_prompt_scores",
+            "gqa_kv_evict_workspace_bytes", "gqa_kv_evict", "gqa_kv_evict_paged",
+            "gqa_kv_append_mxfp4", "gqa_kv_read_mxfp4", "gqa_decode_mxfp4_workspace_bytes", "gqa_decode_mxfp4")
 
 
 class GqaError(RuntimeError):
@@ -80,6 +86,39 @@ def _load():
     lib.gqa_kv_project_append.argtypes = [P, P, P, P, P, I, I, I, I, I, I, P, SZ, I, P]
     lib.gqa_meanpool_kv.restype = I
     lib.gqa_meanpool_kv.argtypes = [P, P, I64, I, I, I64, I, P]
+    D = ctypes.c_double
+    lib.gqa_rope_table.restype = I
+    lib.gqa_rope_table.argtypes = [P, I, I, D, P]
+    lib.gqa_qk_norm_rope.restype = I
+    lib.gqa_qk_norm_rope.argtypes = [P] * 13 + [I] * 6 + [I64] * 3 + [I, I, I, F, I, P]
+    lib.gqa_qk_norm_rope_paged.restype = I
+    lib.gqa_qk_norm_rope_paged.argtypes = [P] * 14 + [I] * 8 + [I64] * 3 + [I, I, I, F, I, P]
+    lib.gqa_decode_scores_workspace_bytes.restype = SZ
+    lib.gqa_decode_scores_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.gqa_decode_scores.restype = I
+    lib.gqa_decode_scores.argtypes = [P, P, P, P, P, P, I, I, I, I, I, F, I, P, SZ, I, P]
+    lib.gqa_decode_scores_paged_workspace_bytes.restype = SZ
+    lib.gqa_decode_scores_paged_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+    lib.gqa_decode_scores_paged.restype = I
+    lib.gqa_decode_scores_paged.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, SZ, I, P]
+    lib.gqa_prompt_scores_workspace_bytes.restype = SZ
+    lib.gqa_prompt_scores_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.gqa_prompt_scores.restype = I
+    lib.gqa_prompt_scores.argtypes = [P, P, P, P, I, I, I, I, I, I, F, P, SZ, I, P]
+    lib.gqa_kv_evict_workspace_bytes.restype = SZ
+    lib.gqa_kv_evict_workspace_bytes.argtypes = [I, I, I, I]
+    lib.gqa_kv_evict.restype = I
+    lib.gqa_kv_evict.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, P, SZ, I, P]
+    lib.gqa_kv_evict_paged.restype = I
+    lib.gqa_kv_evict_paged.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, SZ, I, P]
+    lib.gqa_kv_append_mxfp4.restype = I
+    lib.gqa_kv_append_mxfp4.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P]
+    lib.gqa_kv_read_mxfp4.restype = I
+    lib.gqa_kv_read_mxfp4.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P]
+    lib.gqa_decode_mxfp4_workspace_bytes.restype = SZ
+    lib.gqa_decode_mxfp4_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.gqa_decode_mxfp4.restype = I
+    lib.gqa_decode_mxfp4.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, F, I, P, SZ, P]
     lib.gqa_get_last_error.restype = I
     lib.gqa_get_last_error.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     lib.gqa_status_string.restype = ctypes.c_char_p
@@ -324,3 +363,273 @@ def gqa_get_last_error(stream=None) -> Tuple[int, int]:
     bits = ctypes.c_uint32(0)
     status = _lib.gqa_get_last_error(_stream(stream), ctypes.byref(bits))
     return int(status), int(bits.value)
+
+
+# ---------------------------------------------------------------------------
+# include/gqa_cache.h. These calls run on the device that holds their tensors,
+# whichever device is current, and on that device's current stream.
+
+class _On:
+    """The device all the tensors lie on, made current, and the stream of the call."""
+
+    def __init__(self, stream, *tensors):
+        given = [t for t in tensors if t is not None]
+        if not all(t.is_cuda for t in given):
+            raise ValueError("tensors must be on the GPU")
+        if any(t.device != given[0].device for t in given):
+            raise ValueError("tensors must be on one device")
+        if hasattr(stream, "device") and stream.device != given[0].device:
+            raise ValueError("the stream must be on the tensors' device")
+        self._guard, self._stream = torch.cuda.device(given[0].device), stream
+
+    def __enter__(self):
+        self._guard.__enter__()
+        return _stream(self._stream)
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def _ws(workspace):
+    return workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def _like(t, *others):
+    """Same dtype for all that are given."""
+    assert all(o is None or o.dtype == t.dtype for o in others), "tensors of one call share a dtype"
+
+
+def gqa_rope_table(rope, theta: float = 10000.0, stream=None) -> None:
+    """rope [max_pos, rotary_dim] float32, written: cosines of every position's angles, then their sines."""
+    max_pos, rotary_dim = rope.shape
+    assert rope.dtype == torch.float32
+    with _On(stream, rope) as st:
+        _check("gqa_rope_table", _lib.gqa_rope_table(_ptr(rope), max_pos, rotary_dim, float(theta), st))
+
+
+def _heads(x):
+    """(pointer, token stride) of tokens [B, T, heads, d] whose heads are contiguous; tokens at any one stride."""
+    B, T, n, d = x.shape
+    if not x.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    stride = x.stride(1) if T > 1 else (x.stride(0) if B > 1 else n * d)
+    if x.numel() and (x.stride(3) != 1 or (n > 1 and x.stride(2) != d) or (B > 1 and T > 1 and x.stride(0) != T * stride)):
+        raise ValueError("a token's heads must be contiguous and the tokens at one stride")
+    return ctypes.c_void_p(x.data_ptr()), stride
+
+
+def _norm_rope_args(q_out, q, k, rope, positions, q_weight, k_weight, k_out, v, rows, row_pos, capacity):
+    B, T, H, d = q.shape
+    K = k.shape[2]
+    assert k.shape == (B, T, K, d) and q_out.shape == q.shape and (k_out is None or k_out.shape == k.shape)
+    assert v is None or v.shape == k.shape
+    assert all(w is None or w.shape == (d,) for w in (q_weight, k_weight))
+    assert rope is None or (rope.dtype == torch.float32 and rope.dim() == 2)
+    assert positions is None or (positions.dtype == torch.int32 and positions.shape == (B, T))
+    assert rows is None or (rows.dtype == torch.int32 and rows.shape == (B,))
+    assert row_pos is None or (row_pos.dtype == torch.int32 and row_pos.shape == (B, K, capacity))
+    _like(q, q_out, k, v, k_out, q_weight, k_weight)
+    max_pos, rotary_dim = rope.shape if rope is not None else (0, 0)
+    return B, T, H, K, d, max_pos, rotary_dim
+
+
+def gqa_qk_norm_rope(q_out, q, k, rope, positions, q_weight=None, k_weight=None, eps: float = 1e-6,
+                     interleaved: bool = False, k_out=None, v=None, k_cache=None, v_cache=None, rows=None,
+                     row_pos=None, stream=None) -> None:
+    """Norm each head of q [B,T,H,d] and k [B,T,K,d], rotate by positions [B,T], write q_out, k_out and cache rows.
+
+    q, k, v may be slices of one projection's output (heads contiguous, tokens at one stride). rope
+    [max_pos, rotary_dim] float32 or None; weights [d] or None. Optional: k_out [B,T,K,d]; caches [B,K,S_max,d]
+    with v [B,T,K,d] and rows [B] int32 (row of each sequence's first new token); row_pos [B,K,S_max] int32.
+    """
+    S_max = k_cache.shape[2] if k_cache is not None else (row_pos.shape[2] if row_pos is not None else 0)
+    B, T, H, K, d, max_pos, rd = _norm_rope_args(q_out, q, k, rope, positions, q_weight, k_weight, k_out, v, rows,
+                                                 row_pos, S_max)
+    if k_cache is not None:
+        assert k_cache.shape == (B, K, S_max, d) and v_cache is not None and v_cache.shape == k_cache.shape
+        assert v is not None, "a cache needs v"
+    _like(q, k_cache, v_cache)
+    (qp, qs), (kp, ks), (vp, vs) = _heads(q), _heads(k), (None, K * d) if v is None else _heads(v)
+    with _On(stream, q_out, q, k, rope, positions, q_weight, k_weight, k_out, v, k_cache, v_cache, rows,
+             row_pos) as st:
+        _check("gqa_qk_norm_rope",
+               _lib.gqa_qk_norm_rope(_ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _ptr(row_pos), qp, kp, vp,
+                                     _ptr(q_weight), _ptr(k_weight), _ptr(rope), _ptr(positions), _ptr(rows), B, T, H,
+                                     K, S_max, d, qs, ks, vs, rd, max_pos, int(interleaved), float(eps), _dtype(q),
+                                     st))
+
+
+def gqa_qk_norm_rope_paged(q_out, q, k, v, rope, positions, k_pool, v_pool, block_table, rows, q_weight=None,
+                           k_weight=None, eps: float = 1e-6, interleaved: bool = False, k_out=None, row_pos=None,
+                           stream=None) -> None:
+    """gqa_qk_norm_rope into pools [num_blocks,K,block_size,d] through block_table [B,max_blocks] int32."""
+    nb, Kp, bs, dp = k_pool.shape
+    mb = block_table.shape[1]
+    B, T, H, K, d, max_pos, rd = _norm_rope_args(q_out, q, k, rope, positions, q_weight, k_weight, k_out, v, rows,
+                                                 row_pos, mb * bs)
+    assert (Kp, dp) == (K, d) and v_pool.shape == k_pool.shape
+    assert block_table.dtype == torch.int32 and block_table.shape == (B, mb)
+    _like(q, k_pool, v_pool)
+    (qp, qs), (kp, ks), (vp, vs) = _heads(q), _heads(k), _heads(v)
+    with _On(stream, q_out, q, k, v, rope, positions, k_pool, v_pool, block_table, rows, q_weight, k_weight, k_out,
+             row_pos) as st:
+        _check("gqa_qk_norm_rope_paged",
+               _lib.gqa_qk_norm_rope_paged(_ptr(q_out), _ptr(k_out), _ptr(k_pool), _ptr(v_pool), _ptr(row_pos), qp, kp,
+                                           vp, _ptr(q_weight), _ptr(k_weight), _ptr(rope), _ptr(positions),
+                                           _ptr(block_table), _ptr(rows), B, T, H, K, d, nb, bs, mb, qs, ks, vs, rd,
+                                           max_pos, int(interleaved), float(eps), _dtype(q), st))
+
+
+def gqa_decode_scores_workspace_bytes(B: int, H: int, K: int, S_max: int, d: int, num_splits: int = 0) -> int:
+    return int(_lib.gqa_decode_scores_workspace_bytes(B, H, K, S_max, d, num_splits))
+
+
+def gqa_decode_scores(out, scores, q, k_cache, v_cache, seqlens, scale: float, num_splits: int = 0, workspace=None,
+                      stream=None) -> None:
+    """gqa_decode, and each cached row's attention weight (summed over its group's heads) added to scores [B,K,S_max]."""
+    B, H, d = q.shape
+    _, K, S_max, _ = k_cache.shape
+    assert out.shape == q.shape and k_cache.shape == (B, K, S_max, d) and v_cache.shape == k_cache.shape
+    assert scores.dtype == torch.float32 and scores.shape == (B, K, S_max)
+    assert seqlens.dtype == torch.int32 and seqlens.shape == (B,)
+    _like(q, out, k_cache, v_cache)
+    with _On(stream, out, scores, q, k_cache, v_cache, seqlens, workspace) as st:
+        _check("gqa_decode_scores",
+               _lib.gqa_decode_scores(_ptr(out), _ptr(scores), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seqlens),
+                                      B, H, K, S_max, d, float(scale), int(num_splits), _ptr(workspace),
+                                      _ws(workspace), _dtype(q), st))
+
+
+def gqa_decode_scores_paged_workspace_bytes(B: int, H: int, K: int, d: int, block_size: int, max_blocks: int,
+                                            num_splits: int = 0) -> int:
+    return int(_lib.gqa_decode_scores_paged_workspace_bytes(B, H, K, d, block_size, max_blocks, num_splits))
+
+
+def gqa_decode_scores_paged(out, scores, q, k_pool, v_pool, block_table, seqlens, scale: float, num_splits: int = 0,
+                            workspace=None, stream=None) -> None:
+    """gqa_decode_scores over a paged cache; scores [B,K,max_blocks*block_size] by logical row."""
+    B, H, K, d, nb, bs, mb = _paged_shapes(q, k_pool, v_pool, block_table)
+    assert out.shape == q.shape and seqlens.dtype == torch.int32 and seqlens.shape == (B,)
+    assert scores.dtype == torch.float32 and scores.shape == (B, K, mb * bs)
+    _like(q, out, k_pool, v_pool)
+    with _On(stream, out, scores, q, k_pool, v_pool, block_table, seqlens, workspace) as st:
+        _check("gqa_decode_scores_paged",
+               _lib.gqa_decode_scores_paged(_ptr(out), _ptr(scores), _ptr(q), _ptr(k_pool), _ptr(v_pool),
+                                            _ptr(block_table), _ptr(seqlens), B, H, K, d, nb, bs, mb, float(scale),
+                                            int(num_splits), _ptr(workspace), _ws(workspace), _dtype(q), st))
+
+
+def gqa_prompt_scores_workspace_bytes(B: int, T: int, H: int, K: int, S_max: int, d: int) -> int:
+    return int(_lib.gqa_prompt_scores_workspace_bytes(B, T, H, K, S_max, d))
+
+
+def gqa_prompt_scores(scores, q, k_cache, seqlens, scale: float, workspace=None, stream=None) -> None:
+    """Add the attention weights of the last T tokens' queries q [B,T,H,d] (causal) to scores [B,K,S_max]."""
+    B, T, H, d = q.shape
+    _, K, S_max, _ = k_cache.shape
+    assert k_cache.shape == (B, K, S_max, d) and scores.dtype == torch.float32 and scores.shape == (B, K, S_max)
+    assert seqlens.dtype == torch.int32 and seqlens.shape == (B,)
+    _like(q, k_cache)
+    with _On(stream, scores, q, k_cache, seqlens, workspace) as st:
+        _check("gqa_prompt_scores",
+               _lib.gqa_prompt_scores(_ptr(scores), _ptr(q), _ptr(k_cache), _ptr(seqlens), B, T, H, K, S_max, d,
+                                      float(scale), _ptr(workspace), _ws(workspace), _dtype(q), st))
+
+
+def gqa_kv_evict_workspace_bytes(B: int, K: int, S_max: int, keep: int) -> int:
+    return int(_lib.gqa_kv_evict_workspace_bytes(B, K, S_max, keep))
+
+
+def _evict_args(scores, row_pos, seqlens, recent_from, shape):
+    assert scores.dtype == torch.float32 and scores.shape == shape
+    assert row_pos is None or (row_pos.dtype == torch.int32 and row_pos.shape == shape)
+    assert seqlens.dtype == torch.int32 and seqlens.shape == shape[:1]
+    assert recent_from is None or (recent_from.dtype == torch.int32 and recent_from.shape == shape[:1])
+
+
+def gqa_kv_evict(k_cache, v_cache, scores, row_pos, seqlens, keep: int, sinks: int = 0, recent_from=None,
+                 workspace=None, stream=None) -> None:
+    """Cut every sequence of caches [B,K,S_max,d] to keep rows per KV head: the lowest scores [B,K,S_max] go.
+
+    Rows of position (row_pos [B,K,S_max] int32, or None: their index) below sinks or from recent_from [B] on are
+    held. Everything in place: rows, scores, row_pos, seqlens [B].
+    """
+    B, K, S_max, d = k_cache.shape
+    assert v_cache.shape == k_cache.shape
+    _evict_args(scores, row_pos, seqlens, recent_from, (B, K, S_max))
+    _like(k_cache, v_cache)
+    with _On(stream, k_cache, v_cache, scores, row_pos, seqlens, recent_from, workspace) as st:
+        _check("gqa_kv_evict",
+               _lib.gqa_kv_evict(_ptr(k_cache), _ptr(v_cache), _ptr(scores), _ptr(row_pos), _ptr(seqlens),
+                                 _ptr(recent_from), B, K, S_max, d, int(keep), int(sinks), _ptr(workspace),
+                                 _ws(workspace), _dtype(k_cache), st))
+
+
+def gqa_kv_evict_paged(k_pool, v_pool, block_table, scores, row_pos, seqlens, keep: int, sinks: int = 0,
+                       recent_from=None, workspace=None, stream=None) -> None:
+    """gqa_kv_evict over a paged cache; scores and row_pos are [B,K,max_blocks*block_size], by logical row."""
+    nb, K, bs, d = k_pool.shape
+    B, mb = block_table.shape
+    assert v_pool.shape == k_pool.shape and block_table.dtype == torch.int32
+    _evict_args(scores, row_pos, seqlens, recent_from, (B, K, mb * bs))
+    _like(k_pool, v_pool)
+    with _On(stream, k_pool, v_pool, block_table, scores, row_pos, seqlens, recent_from, workspace) as st:
+        _check("gqa_kv_evict_paged",
+               _lib.gqa_kv_evict_paged(_ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(scores), _ptr(row_pos),
+                                       _ptr(seqlens), _ptr(recent_from), B, K, d, nb, bs, mb, int(keep), int(sinks),
+                                       _ptr(workspace), _ws(workspace), _dtype(k_pool), st))
+
+
+def _mx_shapes(k_codes, k_scales, v_codes, v_scales):
+    B, K, S_max, half = k_codes.shape
+    d = 2 * half
+    assert v_codes.shape == k_codes.shape and k_scales.shape == (B, K, S_max, d // 32)
+    assert v_scales.shape == k_scales.shape
+    assert all(t.dtype == torch.uint8 for t in (k_codes, k_scales, v_codes, v_scales))
+    return B, K, S_max, d
+
+
+def gqa_kv_append_mxfp4(k_codes, k_scales, v_codes, v_scales, k_new, v_new, pos, stream=None) -> None:
+    """Quantize k_new/v_new [B,T,K,d] bf16 into rows pos[b].. of the 4-bit caches (codes [B,K,S_max,d/2], scales
+    [B,K,S_max,d/32], uint8, in place)."""
+    B, K, S_max, d = _mx_shapes(k_codes, k_scales, v_codes, v_scales)
+    T = k_new.shape[1]
+    assert k_new.shape == (B, T, K, d) and v_new.shape == k_new.shape
+    assert k_new.dtype == torch.bfloat16 and v_new.dtype == torch.bfloat16
+    assert pos.dtype == torch.int32 and pos.shape == (B,)
+    with _On(stream, k_codes, k_scales, v_codes, v_scales, k_new, v_new, pos) as st:
+        _check("gqa_kv_append_mxfp4",
+               _lib.gqa_kv_append_mxfp4(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k_new),
+                                        _ptr(v_new), _ptr(pos), B, T, K, S_max, d, st))
+
+
+def gqa_kv_read_mxfp4(k_out, v_out, k_codes, k_scales, v_codes, v_scales, pos, stream=None) -> None:
+    """Rows pos[b].. of the 4-bit caches as k_out/v_out [B,T,K,d] bf16 (exact)."""
+    B, K, S_max, d = _mx_shapes(k_codes, k_scales, v_codes, v_scales)
+    T = k_out.shape[1]
+    assert k_out.shape == (B, T, K, d) and v_out.shape == k_out.shape
+    assert k_out.dtype == torch.bfloat16 and v_out.dtype == torch.bfloat16
+    assert pos.dtype == torch.int32 and pos.shape == (B,)
+    with _On(stream, k_out, v_out, k_codes, k_scales, v_codes, v_scales, pos) as st:
+        _check("gqa_kv_read_mxfp4",
+               _lib.gqa_kv_read_mxfp4(_ptr(k_out), _ptr(v_out), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
+                                      _ptr(v_scales), _ptr(pos), B, T, K, S_max, d, st))
+
+
+def gqa_decode_mxfp4_workspace_bytes(B: int, H: int, K: int, S_max: int, d: int, num_splits: int = 0) -> int:
+    return int(_lib.gqa_decode_mxfp4_workspace_bytes(B, H, K, S_max, d, num_splits))
+
+
+def gqa_decode_mxfp4(out, q, k_codes, k_scales, v_codes, v_scales, seqlens, scale: float, num_splits: int = 0,
+                     workspace=None, stream=None) -> None:
+    """out/q [B,H,d] bf16; codes [B,K,S_max,d/2] and scales [B,K,S_max,d/32] uint8; seqlens [B] int32."""
+    B, H, d = q.shape
+    _, K, S_max, _ = k_codes.shape
+    assert _mx_shapes(k_codes, k_scales, v_codes, v_scales) == (B, K, S_max, d)
+    assert out.shape == q.shape and q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16
+    assert seqlens.dtype == torch.int32 and seqlens.shape == (B,)
+    with _On(stream, out, q, k_codes, k_scales, v_codes, v_scales, seqlens, workspace) as st:
+        _check("gqa_decode_mxfp4",
+               _lib.gqa_decode_mxfp4(_ptr(out), _ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
+                                     _ptr(seqlens), B, H, K, S_max, d, float(scale), int(num_splits),
+                                     _ptr(workspace), _ws(workspace), st))
