@@ -16,27 +16,22 @@ PagedCache paged_cache(const int32_t* table, int num_blocks, int block_size, int
 // ----------------------------------------------------------------------------
 // gqa_qk_norm_rope
 
-// A lane group works through `chunks`-strided rows of a token, R at a time.
 template <typename T, int D>
 int launch_norm_rope(const gqa::NormRopeParams& p0, bool interleaved, int sms, cudaStream_t st) {
-  constexpr int LPR = D / gqa::Vec16<T>::N;
+  constexpr int LPR = D / 8;
   gqa::NormRopeParams p = p0;
   const long long tokens = (long long)p.B * p.T;
   const int rows = p.H + p.K + (p.v_cache ? p.K : 0);
   constexpr int R = 4;
-  // few tokens: a row or so per lane group, as many groups as rows; many: 4 rows, so that one load of the
-  // token's table row serves them
-  const long long threads = (long long)sms * 2048;
-  int per = 1;
-  while (per < R && tokens * ((rows + 2 * per - 1) / (2 * per)) * LPR >= threads) per *= 2;
-  p.chunks = (rows + per - 1) / per;
+  // few tokens: one row per lane group; enough for every SM's threads four times over: R rows, so that one table
+  // row, one position and one address calculation serve them
+  const bool many = tokens * rows * LPR >= (long long)R * sms * 2048;
+  p.chunks = many ? (rows + R - 1) / R : rows;
   const long long groups = tokens * p.chunks;
-  const long long grid = (groups * LPR + gqa::kNrThreads - 1) / gqa::kNrThreads;
-  if (grid >= (1ll << 31)) return GQA_ERR_SHAPE;
-  auto run = [&](auto kernel) {
-    return gqa::launch_kernel(kernel, (unsigned)grid, gqa::kNrThreads, 0, st, true, p);
-  };
-  if (per == 1)
+  if (groups * LPR >= (1ll << 31)) return GQA_ERR_SHAPE;
+  const unsigned grid = (unsigned)((groups * LPR + gqa::kNrThreads - 1) / gqa::kNrThreads);
+  auto run = [&](auto kernel) { return gqa::launch_kernel(kernel, grid, gqa::kNrThreads, 0, st, true, p); };
+  if (!many)
     return interleaved ? run(gqa::qk_norm_rope_kernel<T, D, true, 1>) : run(gqa::qk_norm_rope_kernel<T, D, false, 1>);
   return interleaved ? run(gqa::qk_norm_rope_kernel<T, D, true, R>) : run(gqa::qk_norm_rope_kernel<T, D, false, R>);
 }
@@ -110,7 +105,6 @@ int norm_rope_impl(void* q_out, void* k_out, void* k_cache, void* v_cache, int32
 
 struct ScoresPlan {
   DecodePlan pl;
-  int gp = 0;
   size_t ml_off = 0, queue_off = 0, x_off = 0, bytes = 0;
 };
 
@@ -120,12 +114,11 @@ bool plan_scores(ScoresPlan& sp, int B, int H, int K, int S_max, int d, int num_
   sp.pl = plan_decode(B, H, K, S_max, d, num_splits, GQA_BF16, sms, false, paged, true);
   if (sp.pl.ws_bytes == (size_t)-1) return false;
   const int G = H / K;
-  sp.gp = (G + 1) / 2 * 2;
   const size_t parts = (size_t)B * K * sp.pl.nsplit * G;
   sp.ml_off = sp.pl.nsplit > 1 ? parts * d * sizeof(float) : 0;
   sp.queue_off = (sp.ml_off + parts * sizeof(float2) + 15) / 16 * 16;
   sp.x_off = sp.queue_off + 16;
-  sp.bytes = sp.x_off + (size_t)B * K * S_max * sp.gp * sizeof(float);
+  sp.bytes = sp.x_off + (size_t)B * H * S_max * sizeof(float);
   return true;
 }
 
@@ -200,19 +193,13 @@ int decode_scores_impl(void* out, float* scores, const void* q, const void* k_ca
   gqa::ScoresParams x;
   x.x = reinterpret_cast<float*>(ws + sp.x_off);
   x.scores = scores;
-  x.gp = sp.gp;
   cudaStream_t st = (cudaStream_t)stream;
   const uint64_t rows = pc ? (uint64_t)pc->num_blocks * K * pc->block_size : (uint64_t)B * K * S_max;
   int rc = d == 128 ? launch_scores_decode<128>(sp, p, x, k_cache, v_cache, rows, st)
                     : launch_scores_decode<64>(sp, p, x, k_cache, v_cache, rows, st);
   if (rc != GQA_OK) return rc;
-  if (pl.nsplit > 1) {
-    rc = launch_combine(out, p, seqlens, H, K, S_max, p.G, pl.chunk, pl.nsplit, 1, d, GQA_BF16, pl.nsplit > 32,
-                        (long long)B * H, st);
-    if (rc != GQA_OK) return rc;
-  }
-  return gqa::launch_kernel(gqa::scores_accumulate_kernel, (unsigned)(B * K * chunks), gqa::kAccThreads, 0, st, true,
-                            p, x, (int)chunks);
+  return gqa::launch_kernel(d == 128 ? gqa::scores_finish_kernel<128> : gqa::scores_finish_kernel<64>,
+                            (unsigned)(B * K * chunks), gqa::kAccThreads, 0, st, true, p, x, (int)chunks);
 }
 
 // ----------------------------------------------------------------------------
@@ -314,9 +301,24 @@ int kv_evict_impl(void* k_cache, void* v_cache, float* scores, int32_t* row_pos,
                             true, p);
 }
 
-int mx_grid(long long rows, int sms) {
-  const long long ctas = (rows + gqa::kMxThreads / 16 - 1) / (gqa::kMxThreads / 16);
-  return (int)std::max<long long>(1, std::min<long long>(ctas, (long long)sms * 16));
+// One row of CTAs per sequence and tensor (grid y) for the 4-bit rows' kernels.
+template <typename... KArgs, typename... Args>
+int launch_mx_rows(void (*kernel)(KArgs...), int B, int T, int K, cudaStream_t st, Args... args) {
+  const long long rows = (long long)T * K;
+  if (rows >= (1ll << 31)) return GQA_ERR_SHAPE;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + gqa::kMxBlockRows - 1) / gqa::kMxBlockRows), std::min(2 * B, 65534));
+  cfg.blockDim = dim3(gqa::kMxThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const QueryErrorScope scope;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return GQA_OK;
+  scope.clear_own();
+  return GQA_ERR_CUDA;
 }
 
 // ----------------------------------------------------------------------------
@@ -560,10 +562,9 @@ int gqa_kv_append_mxfp4(uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, u
   if (!aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
       !aligned16(k_new) || !aligned16(v_new))
     return GQA_ERR_ALIGN;
-  return gqa::launch_kernel(gqa::kv_append_mxfp4_kernel,
-                            (unsigned)mx_grid(2ll * B * T * K, sm_count(current_device())), gqa::kMxThreads, 0,
-                            (cudaStream_t)stream, true, k_codes, k_scales, v_codes, v_scales,
-                            static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), pos, B, T, K, S_max);
+  return launch_mx_rows(gqa::kv_append_mxfp4_kernel, B, T, K, (cudaStream_t)stream, k_codes, k_scales, v_codes,
+                        v_scales, static_cast<const uint8_t*>(k_new), static_cast<const uint8_t*>(v_new), pos, B, T, K,
+                        S_max);
 }
 
 int gqa_kv_read_mxfp4(void* k_out, void* v_out, const uint8_t* k_codes, const uint8_t* k_scales,
@@ -577,10 +578,8 @@ int gqa_kv_read_mxfp4(void* k_out, void* v_out, const uint8_t* k_codes, const ui
   if (!aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
       !aligned16(k_out) || !aligned16(v_out))
     return GQA_ERR_ALIGN;
-  return gqa::launch_kernel(gqa::kv_read_mxfp4_kernel,
-                            (unsigned)mx_grid(2ll * B * T * K, sm_count(current_device())), gqa::kMxThreads, 0,
-                            (cudaStream_t)stream, true, static_cast<uint4*>(k_out), static_cast<uint4*>(v_out),
-                            k_codes, k_scales, v_codes, v_scales, pos, B, T, K, S_max);
+  return launch_mx_rows(gqa::kv_read_mxfp4_kernel, B, T, K, (cudaStream_t)stream, static_cast<uint8_t*>(k_out),
+                        static_cast<uint8_t*>(v_out), k_codes, k_scales, v_codes, v_scales, pos, B, T, K, S_max);
 }
 
 size_t gqa_prompt_scores_workspace_bytes(int B, int T, int H, int K, int S_max, int d) {

@@ -6,8 +6,8 @@
 // with x the scaled scores in log2 units and (M, L) the softmax's maximum and
 // sum over all of the sequence's keys. A row's weight is not known before the
 // last split's maximum is, so the decode kernel stores its scaled scores
-// (float32: a weight is as exact as its exponent) and a second kernel turns
-// them into weights once (M, L) of every split are there. Reading K again
+// (float32: a weight is as exact as its exponent), and a second kernel joins
+// the splits: their outputs, and the scores as weights. Reading K again
 // instead would cost 2 d bytes a key; the scores are 8 G bytes a key written
 // and read back, mostly in L2.
 #pragma once
@@ -17,17 +17,16 @@
 namespace gqa {
 
 struct ScoresParams {
-  float* x;       // [B * K, S_max, gp] scaled scores of the group's heads
+  float* x;       // [B * H, S_max] scaled scores
   float* scores;  // [B, K, S_max]
-  int gp;         // G rounded up to even: a lane stores two heads at a time
 };
 
-// warp_tile of decode.cuh, storing the scaled scores of the warp's keys at
-// xrow (the row of key kb in x, at the lane's first head; null: no such head).
+// warp_tile of decode.cuh, storing the scaled scores of the warp's keys: xa, xb
+// are the lane's two heads' scores of key kb (null: no such head).
 template <int D>
 __device__ __forceinline__ void warp_tile_scores(WarpState<D>& st, const uint32_t (&qf)[D / 16][2],
                                                  uint32_t stage_addr, int kb, int rows, int lane, float scale_log2,
-                                                 float* xrow, int gp) {
+                                                 float* xa, float* xb) {
   using C = DecCfg<D>;
   const uint32_t k_base = stage_addr;
   const uint32_t v_base = stage_addr + C::kTileBytes;
@@ -52,10 +51,14 @@ __device__ __forceinline__ void warp_tile_scores(WarpState<D>& st, const uint32_
   const float x1 = v0 ? c[1] * scale_log2 : -INFINITY;
   const float x2 = v1 ? c[2] * scale_log2 : -INFINITY;
   const float x3 = v1 ? c[3] * scale_log2 : -INFINITY;
-  if (xrow != nullptr) {
-    float* dst = xrow + (lane >> 2) * gp;
-    if (v0) *reinterpret_cast<float2*>(dst) = make_float2(x0, x1);
-    if (v1) *reinterpret_cast<float2*>(dst + 8 * gp) = make_float2(x2, x3);
+  const int at = lane >> 2;
+  if (xa != nullptr) {
+    if (v0) xa[at] = x0;
+    if (v1) xa[at + 8] = x2;
+  }
+  if (xb != nullptr) {
+    if (v0) xb[at] = x1;
+    if (v1) xb[at + 8] = x3;
   }
   float mx_a = fmaxf(x0, x2), mx_b = fmaxf(x1, x3);
 #pragma unroll
@@ -251,9 +254,9 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     }
     if (kb < si.rows) {
       const int h = 2 * (lane & 3);
-      float* xrow = h < cur.nh ? sp.x + ((size_t)cur.unit * p.S_max + t0 + kb) * sp.gp + cur.hsl * kDecHeadsPerCta + h
-                               : nullptr;
-      warp_tile_scores<D>(st, qf, smem_u32(smem + s * C::kStageBytes), kb, si.rows, lane, p.scale_log2, xrow, sp.gp);
+      float* x = sp.x + ((size_t)cur.b * p.H + cur.h0 + h) * p.S_max + t0 + kb;
+      warp_tile_scores<D>(st, qf, smem_u32(smem + s * C::kStageBytes), kb, si.rows, lane, p.scale_log2,
+                          h < cur.nh ? x : nullptr, h + 1 < cur.nh ? x + p.S_max : nullptr);
     }
     t0 += kDecTileKeys;
     __syncwarp();
@@ -263,19 +266,25 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   }
 }
 
-// Scores += weights. A CTA takes kAccKeys rows of one unit: its warps first
-// join the splits' (m, l) of the group's heads, then a thread per row adds up
-// the heads' weights in order.
+// The join. A CTA takes kAccKeys rows of one unit. Its warps first join the
+// splits' (m, l) of the group's heads; then a thread per row adds up the
+// heads' weights in order, and the unit's output columns are shared out among
+// the unit's CTAs, a CTA's threads over the splits of its columns (summed in
+// a fixed order).
 constexpr int kAccThreads = 256;
 constexpr int kAccKeys = 1024;
 constexpr int kAccHeads = 64;  // heads whose (M, 1 / L) are held at a time
+constexpr int kAccBatch = 8;   // heads whose scores a thread asks for at once
 
+template <int D>
 __global__ void __launch_bounds__(kAccThreads)
-    scores_accumulate_kernel(const DecodeParams p, const ScoresParams sp, int chunks) {
+    scores_finish_kernel(const DecodeParams p, const ScoresParams sp, int chunks) {
   __shared__ float2 ml[kAccHeads];
-  const int unit = blockIdx.x / chunks;
-  const int b = unit / p.K;
-  const int k0 = (blockIdx.x % chunks) * kAccKeys;
+  __shared__ float4 red[kAccThreads];
+  constexpr int J = kAccKeys / kAccThreads;
+  const int unit = blockIdx.x / chunks, part = blockIdx.x % chunks;
+  const int b = unit / p.K, g = unit % p.K;
+  const int k0 = part * kAccKeys;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_wait();
   grid_dep_launch();
@@ -283,41 +292,99 @@ __global__ void __launch_bounds__(kAccThreads)
   const int n = min(kAccKeys, len - k0);
   if (n <= 0) return;
   const int ns = (len + p.chunk - 1) / p.chunk;
-  float acc[kAccKeys / kAccThreads];
+  const int active = (len + kAccKeys - 1) / kAccKeys;  // CTAs of the unit that have rows
+  // the output columns of this CTA, four dims each
+  const int cols = p.G * (D / 4), per = (cols + active - 1) / active;
+  const float* x0 = sp.x + ((size_t)b * p.H + (size_t)g * p.G) * p.S_max + k0 + tid;
+  float acc[J];
 #pragma unroll
-  for (int j = 0; j < kAccKeys / kAccThreads; ++j) acc[j] = 0.f;
+  for (int j = 0; j < J; ++j) acc[j] = 0.f;
   for (int h0 = 0; h0 < p.G; h0 += kAccHeads) {
     const int nh = min(kAccHeads, p.G - h0);
-    __syncthreads();
-    for (int h = warp; h < nh; h += kAccThreads / 32) {
-      const float2* part = p.ws_ml + (size_t)unit * p.nsplit * p.G + h0 + h;
-      float M = -INFINITY, L = 0.f;
-      for (int s = lane; s < ns; s += 32) M = fmaxf(M, __ldcg(&part[(size_t)s * p.G].x));
+    float x[kAccBatch][J];
+    auto ask = [&](int h) {
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      for (int i = 0; i < kAccBatch; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          x[i][j] = h + i < nh && tid + j * kAccThreads < n
+                        ? __ldcg(x0 + (size_t)(h0 + h + i) * p.S_max + j * kAccThreads)
+                        : -INFINITY;
+    };
+    ask(0);
+    if (h0 > 0) __syncthreads();
+    for (int h = warp; h < nh; h += kAccThreads / 32) {
+      const float2* ptr = p.ws_ml + (size_t)unit * p.nsplit * p.G + h0 + h;
+      float M = -INFINITY, L = 0.f;
+#pragma unroll 4
       for (int s = lane; s < ns; s += 32) {
-        const float2 m = __ldcg(&part[(size_t)s * p.G]);
-        L += m.y * fast_exp2(m.x - M);
+        const float2 v = __ldcg(&ptr[(size_t)s * p.G]);
+        const float mn = fmaxf(M, v.x);
+        L = L * fast_exp2(M - mn) + v.y * fast_exp2(v.x - mn);
+        M = mn;
       }
+      float top = M;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      L = M == -INFINITY ? L : L * fast_exp2(M - top);  // a lane without splits holds 0
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-      if (lane == 0) ml[h] = make_float2(M, 1.f / L);
+      if (lane == 0) ml[h] = make_float2(top, 1.f / L);
     }
     __syncthreads();
+    for (int h = 0; h < nh; h += kAccBatch) {
+      if (h > 0) ask(h);
 #pragma unroll
-    for (int j = 0; j < kAccKeys / kAccThreads; ++j) {
-      const int i = tid + j * kAccThreads;
-      if (i >= n) continue;
-      const float2* x = reinterpret_cast<const float2*>(sp.x + ((size_t)unit * p.S_max + k0 + i) * sp.gp + h0);
-      for (int h = 0; h < nh; h += 2) {
-        const float2 v = __ldcg(x + h / 2);
-        acc[j] += fast_exp2(v.x - ml[h].x) * ml[h].y;
-        if (h + 1 < nh) acc[j] += fast_exp2(v.y - ml[h + 1].x) * ml[h + 1].y;
+      for (int i = 0; i < kAccBatch; ++i) {
+        if (h + i < nh) {
+          const float2 z = ml[h + i];
+#pragma unroll
+          for (int j = 0; j < J; ++j) acc[j] = fmaf(fast_exp2(x[i][j] - z.x), z.y, acc[j]);
+        }
+      }
+    }
+    if (ns > 1) {
+      // columns of heads h0 .. h0 + nh - 1
+      const int c0 = max(part * per, h0 * (D / 4)), c1 = min(min(part * per + per, cols), (h0 + nh) * (D / 4));
+      int width = 1;  // columns at a time: a power of two, so that as many threads as possible share the splits
+      while (width < min(c1 - c0, kAccThreads)) width *= 2;
+      const int slots = kAccThreads / width;
+      const int cc = tid % width, slot = tid / width;
+      for (int c = c0; c < c1; c += width) {
+        const int col = c + cc;
+        const int h = col / (D / 4);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col < c1) {
+          const float top = ml[h - h0].x;
+          const size_t base = (size_t)unit * p.nsplit * p.G + h;
+          const float4* src = reinterpret_cast<const float4*>(p.ws_o + base * D) + (col - h * (D / 4));
+#pragma unroll 4
+          for (int s = slot; s < ns; s += slots) {
+            const float f = fast_exp2(__ldcg(&p.ws_ml[base + (size_t)s * p.G].x) - top);
+            const float4 v = __ldcg(src + (size_t)s * p.G * (D / 4));
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z);
+            o.w = fmaf(v.w, f, o.w);
+          }
+        }
+        red[tid] = o;
+        __syncthreads();
+        if (slot == 0 && col < c1) {
+          for (int s = 1; s < slots; ++s) {
+            const float4 v = red[s * width + cc];
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+          }
+          const float inv = ml[h - h0].y;
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + ((size_t)b * p.H + g * p.G) * D + col * 4) =
+              make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        }
+        __syncthreads();
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < kAccKeys / kAccThreads; ++j) {
+  for (int j = 0; j < J; ++j) {
     const int i = tid + j * kAccThreads;
     if (i < n) sp.scores[(size_t)unit * p.S_max + k0 + i] += acc[j];
   }

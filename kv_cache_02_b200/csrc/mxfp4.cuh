@@ -5,8 +5,11 @@
 // the values' bits but for the one rounding of the code, which the hardware's
 // conversion makes (nearest, ties to even, saturating).
 //
-// Streams: 16 lanes hold one row of 128 (8 values, one 16-byte access each),
-// so a block is 4 lanes and its maximum two shuffles.
+// Streams: 8 lanes hold one row of 128, the 8 values of 16-byte chunk l and
+// those of chunk l + 8 in lane l, so that every access is contiguous over the
+// lanes and a block is four lanes; a lane group has kMxUnroll rows in flight.
+// The grid's y dimension is sequence and tensor: one division by K is all the
+// index arithmetic of a row.
 #pragma once
 
 #include "common.cuh"
@@ -37,60 +40,76 @@ __device__ __forceinline__ float e8m0_value(uint32_t e) {
   return e == 0 ? __uint_as_float(0x00400000u) : e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(e << 23);
 }
 
-// Row index r of the call (K rows of all tokens, then V rows) -> tensor, token, head.
+constexpr int kMxLanes = 8;    // lanes of a row
+constexpr int kMxUnroll = 4;   // rows of a lane group
+constexpr int kMxBlockRows = kMxThreads / kMxLanes * kMxUnroll;
+
+// blockIdx.y: 2 b for K, 2 b + 1 for V; rows t * K + g of the sequence
 __global__ void __launch_bounds__(kMxThreads)
     kv_append_mxfp4_kernel(uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales,
-                           const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+                           const uint8_t* __restrict__ k_new, const uint8_t* __restrict__ v_new,
                            const int32_t* __restrict__ pos, int B, int T, int K, int S_max) {
   grid_dep_wait();
   grid_dep_launch();
-  const long long nrows = (long long)B * T * K;
-  const int l = threadIdx.x & 15;
-  const long long per_round = (long long)gridDim.x * (kMxThreads / 16);
-  const long long rounds = (2 * nrows + per_round - 1) / per_round;
-  for (long long it = 0; it < rounds; ++it) {
-    const long long r = it * per_round + blockIdx.x * (long long)(kMxThreads / 16) + (threadIdx.x >> 4);
-    const bool live = r < 2 * nrows;
-    const bool is_v = r >= nrows;
-    const long long row = live ? (is_v ? r - nrows : r) : 0;  // (b * T + t) * K + g
-    const int g = (int)(row % K);
-    const long long n = row / K;
-    const int t = (int)(n % T), b = (int)(n / T);
+  const unsigned nrows = (unsigned)T * (unsigned)K;
+  const int l = threadIdx.x % kMxLanes;
+  const unsigned r0 = blockIdx.x * (unsigned)kMxBlockRows + threadIdx.x / kMxLanes;
+  for (int y = blockIdx.y; y < 2 * B; y += gridDim.y) {
+    const bool is_v = y & 1;
+    const int b = y >> 1;
     const int p0 = __ldg(pos + b);
-    const uint4 w = live ? __ldg((is_v ? v_new : k_new) + row * 16 + l) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    float x[8];
-    uint32_t top = 0;  // the block's largest magnitude, as bits: a NaN's are above infinity's
+    const uint4* src = reinterpret_cast<const uint4*>((is_v ? v_new : k_new) + (size_t)b * nrows * (2 * kMxD)) + l;
+    uint4 w[kMxUnroll][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      top = max(top, max((u[i] << 16) & 0x7fffffffu, u[i] & 0x7fff0000u));
+    for (int i = 0; i < kMxUnroll; ++i) {
+      const unsigned r = r0 + i * (kMxThreads / kMxLanes);
+      w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < nrows) {
+        w[i][0] = __ldg(src + (size_t)r * 16);
+        w[i][1] = __ldg(src + (size_t)r * 16 + 8);
+      }
     }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const bool bad = top >= 0x7f800000u;
-    const uint32_t e = bad ? 255u : (uint32_t)max((int)(top >> 23) - 2, 0);
-    const float inv = bad ? 0.f : __uint_as_float((254u - e) << 23);  // 2^(127 - E), exact
+    const bool fits = p0 >= 0 && p0 <= S_max - T;
+    if (!fits && !is_v && blockIdx.x == 0 && threadIdx.x == 0) raise_error(GQA_DEVERR_APPEND_POS);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = bad ? 0.f : x[i] * inv;
-    const uint32_t codes = e2m1x8(x);
-    // the row's four scales in lane 0 of the 16
-    uint32_t sc = e;
-    sc |= __shfl_down_sync(0xffffffffu, sc, 4, 16) << 8;   // lanes 0, 8: two scales
-    sc |= __shfl_down_sync(0xffffffffu, sc, 8, 16) << 16;  // lane 0: four
-    if (!live) continue;
-    if (p0 < 0 || p0 > S_max - T) {
-      if (l == 0 && !is_v && g == 0 && t == 0) raise_error(GQA_DEVERR_APPEND_POS);
-      continue;
+    for (int i = 0; i < kMxUnroll; ++i) {
+      const unsigned r = r0 + i * (kMxThreads / kMxLanes);
+      uint32_t codes[2], e[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t u[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
+        uint32_t top = 0;  // the block's largest magnitude, as bits: a NaN's are above infinity's
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max((u[j] << 16) & 0x7fffffffu, u[j] & 0x7fff0000u));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const bool bad = top >= 0x7f800000u;
+        e[h] = bad ? 255u : (uint32_t)max((int)(top >> 23) - 2, 0);
+        const float inv = bad ? 0.f : __uint_as_float((254u - e[h]) << 23);  // 2^(127 - E), exact
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[2 * j] = bad ? 0.f : __uint_as_float(u[j] << 16) * inv;
+          x[2 * j + 1] = bad ? 0.f : __uint_as_float(u[j] & 0xffff0000u) * inv;
+        }
+        codes[h] = e2m1x8(x);
+      }
+      // the row's four scales in lane 0: blocks 0, 2 are its own, 1, 3 those of lane 4
+      uint32_t sc = e[0] | (e[1] << 16);
+      sc |= __shfl_down_sync(0xffffffffu, sc, 4, kMxLanes) << 8;
+      if (r < nrows && fits) {
+        const unsigned t = r / (unsigned)K, g = r - t * (unsigned)K;
+        const size_t dst = ((size_t)b * K + g) * S_max + p0 + t;
+        uint32_t* row = reinterpret_cast<uint32_t*>((is_v ? v_codes : k_codes) + dst * kMxRowBytes);
+        row[l] = codes[0];
+        row[l + 8] = codes[1];
+        if (l == 0) reinterpret_cast<uint32_t*>(is_v ? v_scales : k_scales)[dst] = sc;
+      }
     }
-    const long long dst = ((long long)b * K + g) * S_max + p0 + t;
-    reinterpret_cast<uint32_t*>((is_v ? v_codes : k_codes) + dst * kMxRowBytes)[l] = codes;
-    if (l == 0) reinterpret_cast<uint32_t*>(is_v ? v_scales : k_scales)[dst] = sc;
   }
 }
 
-// 8 e2m1 codes -> bf16 values times the scale, exact
+// 8 e2m1 codes times the scale -> bf16 values, exact
 __device__ __forceinline__ uint4 mx_values8(uint32_t codes, float scale) {
   uint32_t out[4];
 #pragma unroll
@@ -109,32 +128,45 @@ __device__ __forceinline__ uint4 mx_values8(uint32_t codes, float scale) {
 }
 
 __global__ void __launch_bounds__(kMxThreads)
-    kv_read_mxfp4_kernel(uint4* __restrict__ k_out, uint4* __restrict__ v_out, const uint8_t* __restrict__ k_codes,
+    kv_read_mxfp4_kernel(uint8_t* __restrict__ k_out, uint8_t* __restrict__ v_out, const uint8_t* __restrict__ k_codes,
                          const uint8_t* __restrict__ k_scales, const uint8_t* __restrict__ v_codes,
                          const uint8_t* __restrict__ v_scales, const int32_t* __restrict__ pos, int B, int T, int K,
                          int S_max) {
   grid_dep_wait();
   grid_dep_launch();
-  const long long nrows = (long long)B * T * K;
-  const int l = threadIdx.x & 15;
-  const long long per_round = (long long)gridDim.x * (kMxThreads / 16);
-  for (long long r = blockIdx.x * (long long)(kMxThreads / 16) + (threadIdx.x >> 4); r < 2 * nrows; r += per_round) {
-    const bool is_v = r >= nrows;
-    const long long row = is_v ? r - nrows : r;
-    const int g = (int)(row % K);
-    const long long n = row / K;
-    const int t = (int)(n % T), b = (int)(n / T);
+  const unsigned nrows = (unsigned)T * (unsigned)K;
+  const int l = threadIdx.x % kMxLanes;
+  const unsigned r0 = blockIdx.x * (unsigned)kMxBlockRows + threadIdx.x / kMxLanes;
+  for (int y = blockIdx.y; y < 2 * B; y += gridDim.y) {
+    const bool is_v = y & 1;
+    const int b = y >> 1;
     const int p0 = __ldg(pos + b);
-    uint4 val = make_uint4(0u, 0u, 0u, 0u);
-    if (p0 < 0 || p0 > S_max - T) {
-      if (l == 0 && !is_v && g == 0 && t == 0) raise_error(GQA_DEVERR_APPEND_POS);
-    } else {
-      const long long src = ((long long)b * K + g) * S_max + p0 + t;
-      const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>((is_v ? v_codes : k_codes) + src * kMxRowBytes) + l);
-      const uint32_t sc = __ldg(reinterpret_cast<const uint32_t*>(is_v ? v_scales : k_scales) + src);
-      val = mx_values8(codes, e8m0_value((sc >> (8 * (l >> 2))) & 255u));
+    const bool fits = p0 >= 0 && p0 <= S_max - T;
+    if (!fits && !is_v && blockIdx.x == 0 && threadIdx.x == 0) raise_error(GQA_DEVERR_APPEND_POS);
+    uint4* out = reinterpret_cast<uint4*>((is_v ? v_out : k_out) + (size_t)b * nrows * (2 * kMxD)) + l;
+    uint32_t codes[kMxUnroll][2], sc[kMxUnroll];
+#pragma unroll
+    for (int i = 0; i < kMxUnroll; ++i) {
+      const unsigned r = r0 + i * (kMxThreads / kMxLanes);
+      codes[i][0] = codes[i][1] = 0u;
+      sc[i] = 0x7f7f7f7fu;
+      if (r < nrows && fits) {
+        const unsigned t = r / (unsigned)K, g = r - t * (unsigned)K;
+        const size_t at = ((size_t)b * K + g) * S_max + p0 + t;
+        const uint32_t* row = reinterpret_cast<const uint32_t*>((is_v ? v_codes : k_codes) + at * kMxRowBytes);
+        codes[i][0] = __ldg(row + l);
+        codes[i][1] = __ldg(row + l + 8);
+        sc[i] = __ldg(reinterpret_cast<const uint32_t*>(is_v ? v_scales : k_scales) + at);
+      }
     }
-    (is_v ? v_out : k_out)[row * 16 + l] = val;
+#pragma unroll
+    for (int i = 0; i < kMxUnroll; ++i) {
+      const unsigned r = r0 + i * (kMxThreads / kMxLanes);
+      if (r >= nrows) continue;
+      const uint32_t mine = sc[i] >> (8 * (l >> 2));  // blocks l / 4 and l / 4 + 2
+      out[(size_t)r * 16] = mx_values8(codes[i][0], e8m0_value(mine & 255u));
+      out[(size_t)r * 16 + 8] = mx_values8(codes[i][1], e8m0_value((mine >> 16) & 255u));
+    }
   }
 }
 

@@ -367,55 +367,75 @@ def gqa_get_last_error(stream=None) -> Tuple[int, int]:
 
 # ---------------------------------------------------------------------------
 # include/gqa_cache.h. These calls run on the device that holds their tensors,
-# whichever device is current, and on that device's current stream.
+# whichever device is current, and on that device's current stream. A call of
+# these few microseconds is bound by its host time, so each argument is looked
+# at once and the stream comes as its raw handle (current_stream() builds an
+# object: 3 us of a call's 7 to 10).
 
-class _On:
-    """The device all the tensors lie on, made current, and the stream of the call."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, stream, *tensors):
-        given = [t for t in tensors if t is not None]
-        if not all(t.is_cuda for t in given):
-            raise ValueError("tensors must be on the GPU")
-        if any(t.device != given[0].device for t in given):
-            raise ValueError("tensors must be on one device")
-        if hasattr(stream, "device") and stream.device != given[0].device:
+
+def _call(name, tensors, scalars, stream, strided=0, after=None) -> None:
+    """The library's `name` on the device pointers of tensors (contiguous, but for the bits of strided; all on one
+    device), then scalars, then the stream. With `after` the last tensor is a workspace: its pointer and size come
+    behind the scalars, then `after`."""
+    dev = None
+    ptrs = []
+    for i, t in enumerate(tensors):
+        if t is None:
+            ptrs.append(None)
+            continue
+        at = t.get_device()
+        if at != dev:
+            if at < 0:
+                raise ValueError("tensors must be on the GPU")
+            if dev is not None:
+                raise ValueError("tensors must be on one device")
+            dev = at
+        if not (strided >> i & 1 or t.is_contiguous()):
+            raise ValueError("tensors must be contiguous")
+        ptrs.append(t.data_ptr())
+    if after is not None:
+        scalars = (*scalars, ptrs.pop(), 0 if tensors[-1] is None else tensors[-1].nbytes, *after)
+    if stream is None:
+        handle = _raw_stream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        if stream.device.index != dev:
             raise ValueError("the stream must be on the tensors' device")
-        self._guard, self._stream = torch.cuda.device(given[0].device), stream
-
-    def __enter__(self):
-        self._guard.__enter__()
-        return _stream(self._stream)
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
-
-
-def _ws(workspace):
-    return workspace.numel() * workspace.element_size() if workspace is not None else 0
+        handle = stream.cuda_stream
+    else:
+        handle = int(stream)
+    if dev == torch.cuda.current_device():
+        status = getattr(_lib, name)(*ptrs, *scalars, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib, name)(*ptrs, *scalars, handle)
+    if status != GQA_OK:
+        raise GqaError(name, status)
 
 
 def _like(t, *others):
     """Same dtype for all that are given."""
-    assert all(o is None or o.dtype == t.dtype for o in others), "tensors of one call share a dtype"
+    dtype = t.dtype
+    for o in others:
+        assert o is None or o.dtype == dtype, "tensors of one call share a dtype"
 
 
 def gqa_rope_table(rope, theta: float = 10000.0, stream=None) -> None:
     """rope [max_pos, rotary_dim] float32, written: cosines of every position's angles, then their sines."""
     max_pos, rotary_dim = rope.shape
     assert rope.dtype == torch.float32
-    with _On(stream, rope) as st:
-        _check("gqa_rope_table", _lib.gqa_rope_table(_ptr(rope), max_pos, rotary_dim, float(theta), st))
+    _call("gqa_rope_table", (rope,), (max_pos, rotary_dim, float(theta)), stream)
 
 
-def _heads(x):
-    """(pointer, token stride) of tokens [B, T, heads, d] whose heads are contiguous; tokens at any one stride."""
+def _token_stride(x):
+    """Token stride of tokens [B, T, heads, d] whose heads are contiguous; tokens at any one stride."""
     B, T, n, d = x.shape
-    if not x.is_cuda:
-        raise ValueError("tensors must be on the GPU")
-    stride = x.stride(1) if T > 1 else (x.stride(0) if B > 1 else n * d)
-    if x.numel() and (x.stride(3) != 1 or (n > 1 and x.stride(2) != d) or (B > 1 and T > 1 and x.stride(0) != T * stride)):
+    sb, st, sn, sd = x.stride()
+    stride = st if T > 1 else (sb if B > 1 else n * d)
+    if (sd != 1 or (n > 1 and sn != d) or (B > 1 and T > 1 and sb != T * stride)) and x.numel():
         raise ValueError("a token's heads must be contiguous and the tokens at one stride")
-    return ctypes.c_void_p(x.data_ptr()), stride
+    return stride
 
 
 def _norm_rope_args(q_out, q, k, rope, positions, q_weight, k_weight, k_out, v, rows, row_pos, capacity):
@@ -423,7 +443,7 @@ def _norm_rope_args(q_out, q, k, rope, positions, q_weight, k_weight, k_out, v, 
     K = k.shape[2]
     assert k.shape == (B, T, K, d) and q_out.shape == q.shape and (k_out is None or k_out.shape == k.shape)
     assert v is None or v.shape == k.shape
-    assert all(w is None or w.shape == (d,) for w in (q_weight, k_weight))
+    assert (q_weight is None or q_weight.shape == (d,)) and (k_weight is None or k_weight.shape == (d,))
     assert rope is None or (rope.dtype == torch.float32 and rope.dim() == 2)
     assert positions is None or (positions.dtype == torch.int32 and positions.shape == (B, T))
     assert rows is None or (rows.dtype == torch.int32 and rows.shape == (B,))
@@ -448,15 +468,11 @@ def gqa_qk_norm_rope(q_out, q, k, rope, positions, q_weight=None, k_weight=None,
     if k_cache is not None:
         assert k_cache.shape == (B, K, S_max, d) and v_cache is not None and v_cache.shape == k_cache.shape
         assert v is not None, "a cache needs v"
-    _like(q, k_cache, v_cache)
-    (qp, qs), (kp, ks), (vp, vs) = _heads(q), _heads(k), (None, K * d) if v is None else _heads(v)
-    with _On(stream, q_out, q, k, rope, positions, q_weight, k_weight, k_out, v, k_cache, v_cache, rows,
-             row_pos) as st:
-        _check("gqa_qk_norm_rope",
-               _lib.gqa_qk_norm_rope(_ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _ptr(row_pos), qp, kp, vp,
-                                     _ptr(q_weight), _ptr(k_weight), _ptr(rope), _ptr(positions), _ptr(rows), B, T, H,
-                                     K, S_max, d, qs, ks, vs, rd, max_pos, int(interleaved), float(eps), _dtype(q),
-                                     st))
+        _like(q, k_cache, v_cache)
+    _call("gqa_qk_norm_rope",
+          (q_out, k_out, k_cache, v_cache, row_pos, q, k, v, q_weight, k_weight, rope, positions, rows),
+          (B, T, H, K, S_max, d, _token_stride(q), _token_stride(k), K * d if v is None else _token_stride(v), rd,
+           max_pos, int(interleaved), float(eps), _dtype(q)), stream, strided=0b11100000)
 
 
 def gqa_qk_norm_rope_paged(q_out, q, k, v, rope, positions, k_pool, v_pool, block_table, rows, q_weight=None,
@@ -467,17 +483,13 @@ def gqa_qk_norm_rope_paged(q_out, q, k, v, rope, positions, k_pool, v_pool, bloc
     mb = block_table.shape[1]
     B, T, H, K, d, max_pos, rd = _norm_rope_args(q_out, q, k, rope, positions, q_weight, k_weight, k_out, v, rows,
                                                  row_pos, mb * bs)
-    assert (Kp, dp) == (K, d) and v_pool.shape == k_pool.shape
+    assert Kp == K and dp == d and v_pool.shape == k_pool.shape
     assert block_table.dtype == torch.int32 and block_table.shape == (B, mb)
     _like(q, k_pool, v_pool)
-    (qp, qs), (kp, ks), (vp, vs) = _heads(q), _heads(k), _heads(v)
-    with _On(stream, q_out, q, k, v, rope, positions, k_pool, v_pool, block_table, rows, q_weight, k_weight, k_out,
-             row_pos) as st:
-        _check("gqa_qk_norm_rope_paged",
-               _lib.gqa_qk_norm_rope_paged(_ptr(q_out), _ptr(k_out), _ptr(k_pool), _ptr(v_pool), _ptr(row_pos), qp, kp,
-                                           vp, _ptr(q_weight), _ptr(k_weight), _ptr(rope), _ptr(positions),
-                                           _ptr(block_table), _ptr(rows), B, T, H, K, d, nb, bs, mb, qs, ks, vs, rd,
-                                           max_pos, int(interleaved), float(eps), _dtype(q), st))
+    _call("gqa_qk_norm_rope_paged",
+          (q_out, k_out, k_pool, v_pool, row_pos, q, k, v, q_weight, k_weight, rope, positions, block_table, rows),
+          (B, T, H, K, d, nb, bs, mb, _token_stride(q), _token_stride(k), _token_stride(v), rd, max_pos,
+           int(interleaved), float(eps), _dtype(q)), stream, strided=0b11100000)
 
 
 def gqa_decode_scores_workspace_bytes(B: int, H: int, K: int, S_max: int, d: int, num_splits: int = 0) -> int:
@@ -493,11 +505,8 @@ def gqa_decode_scores(out, scores, q, k_cache, v_cache, seqlens, scale: float, n
     assert scores.dtype == torch.float32 and scores.shape == (B, K, S_max)
     assert seqlens.dtype == torch.int32 and seqlens.shape == (B,)
     _like(q, out, k_cache, v_cache)
-    with _On(stream, out, scores, q, k_cache, v_cache, seqlens, workspace) as st:
-        _check("gqa_decode_scores",
-               _lib.gqa_decode_scores(_ptr(out), _ptr(scores), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seqlens),
-                                      B, H, K, S_max, d, float(scale), int(num_splits), _ptr(workspace),
-                                      _ws(workspace), _dtype(q), st))
+    _call("gqa_decode_scores", (out, scores, q, k_cache, v_cache, seqlens, workspace),
+          (B, H, K, S_max, d, float(scale), int(num_splits)), stream, after=(_dtype(q),))
 
 
 def gqa_decode_scores_paged_workspace_bytes(B: int, H: int, K: int, d: int, block_size: int, max_blocks: int,
@@ -512,11 +521,8 @@ def gqa_decode_scores_paged(out, scores, q, k_pool, v_pool, block_table, seqlens
     assert out.shape == q.shape and seqlens.dtype == torch.int32 and seqlens.shape == (B,)
     assert scores.dtype == torch.float32 and scores.shape == (B, K, mb * bs)
     _like(q, out, k_pool, v_pool)
-    with _On(stream, out, scores, q, k_pool, v_pool, block_table, seqlens, workspace) as st:
-        _check("gqa_decode_scores_paged",
-               _lib.gqa_decode_scores_paged(_ptr(out), _ptr(scores), _ptr(q), _ptr(k_pool), _ptr(v_pool),
-                                            _ptr(block_table), _ptr(seqlens), B, H, K, d, nb, bs, mb, float(scale),
-                                            int(num_splits), _ptr(workspace), _ws(workspace), _dtype(q), st))
+    _call("gqa_decode_scores_paged", (out, scores, q, k_pool, v_pool, block_table, seqlens, workspace),
+          (B, H, K, d, nb, bs, mb, float(scale), int(num_splits)), stream, after=(_dtype(q),))
 
 
 def gqa_prompt_scores_workspace_bytes(B: int, T: int, H: int, K: int, S_max: int, d: int) -> int:
@@ -530,10 +536,8 @@ def gqa_prompt_scores(scores, q, k_cache, seqlens, scale: float, workspace=None,
     assert k_cache.shape == (B, K, S_max, d) and scores.dtype == torch.float32 and scores.shape == (B, K, S_max)
     assert seqlens.dtype == torch.int32 and seqlens.shape == (B,)
     _like(q, k_cache)
-    with _On(stream, scores, q, k_cache, seqlens, workspace) as st:
-        _check("gqa_prompt_scores",
-               _lib.gqa_prompt_scores(_ptr(scores), _ptr(q), _ptr(k_cache), _ptr(seqlens), B, T, H, K, S_max, d,
-                                      float(scale), _ptr(workspace), _ws(workspace), _dtype(q), st))
+    _call("gqa_prompt_scores", (scores, q, k_cache, seqlens, workspace), (B, T, H, K, S_max, d, float(scale)), stream,
+          after=(_dtype(q),))
 
 
 def gqa_kv_evict_workspace_bytes(B: int, K: int, S_max: int, keep: int) -> int:
@@ -558,11 +562,8 @@ def gqa_kv_evict(k_cache, v_cache, scores, row_pos, seqlens, keep: int, sinks: i
     assert v_cache.shape == k_cache.shape
     _evict_args(scores, row_pos, seqlens, recent_from, (B, K, S_max))
     _like(k_cache, v_cache)
-    with _On(stream, k_cache, v_cache, scores, row_pos, seqlens, recent_from, workspace) as st:
-        _check("gqa_kv_evict",
-               _lib.gqa_kv_evict(_ptr(k_cache), _ptr(v_cache), _ptr(scores), _ptr(row_pos), _ptr(seqlens),
-                                 _ptr(recent_from), B, K, S_max, d, int(keep), int(sinks), _ptr(workspace),
-                                 _ws(workspace), _dtype(k_cache), st))
+    _call("gqa_kv_evict", (k_cache, v_cache, scores, row_pos, seqlens, recent_from, workspace),
+          (B, K, S_max, d, int(keep), int(sinks)), stream, after=(_dtype(k_cache),))
 
 
 def gqa_kv_evict_paged(k_pool, v_pool, block_table, scores, row_pos, seqlens, keep: int, sinks: int = 0,
@@ -573,11 +574,8 @@ def gqa_kv_evict_paged(k_pool, v_pool, block_table, scores, row_pos, seqlens, ke
     assert v_pool.shape == k_pool.shape and block_table.dtype == torch.int32
     _evict_args(scores, row_pos, seqlens, recent_from, (B, K, mb * bs))
     _like(k_pool, v_pool)
-    with _On(stream, k_pool, v_pool, block_table, scores, row_pos, seqlens, recent_from, workspace) as st:
-        _check("gqa_kv_evict_paged",
-               _lib.gqa_kv_evict_paged(_ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(scores), _ptr(row_pos),
-                                       _ptr(seqlens), _ptr(recent_from), B, K, d, nb, bs, mb, int(keep), int(sinks),
-                                       _ptr(workspace), _ws(workspace), _dtype(k_pool), st))
+    _call("gqa_kv_evict_paged", (k_pool, v_pool, block_table, scores, row_pos, seqlens, recent_from, workspace),
+          (B, K, d, nb, bs, mb, int(keep), int(sinks)), stream, after=(_dtype(k_pool),))
 
 
 def _mx_shapes(k_codes, k_scales, v_codes, v_scales):
@@ -585,7 +583,8 @@ def _mx_shapes(k_codes, k_scales, v_codes, v_scales):
     d = 2 * half
     assert v_codes.shape == k_codes.shape and k_scales.shape == (B, K, S_max, d // 32)
     assert v_scales.shape == k_scales.shape
-    assert all(t.dtype == torch.uint8 for t in (k_codes, k_scales, v_codes, v_scales))
+    _like(k_codes, k_scales, v_codes, v_scales)
+    assert k_codes.dtype == torch.uint8
     return B, K, S_max, d
 
 
@@ -597,10 +596,7 @@ def gqa_kv_append_mxfp4(k_codes, k_scales, v_codes, v_scales, k_new, v_new, pos,
     assert k_new.shape == (B, T, K, d) and v_new.shape == k_new.shape
     assert k_new.dtype == torch.bfloat16 and v_new.dtype == torch.bfloat16
     assert pos.dtype == torch.int32 and pos.shape == (B,)
-    with _On(stream, k_codes, k_scales, v_codes, v_scales, k_new, v_new, pos) as st:
-        _check("gqa_kv_append_mxfp4",
-               _lib.gqa_kv_append_mxfp4(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k_new),
-                                        _ptr(v_new), _ptr(pos), B, T, K, S_max, d, st))
+    _call("gqa_kv_append_mxfp4", (k_codes, k_scales, v_codes, v_scales, k_new, v_new, pos), (B, T, K, S_max, d), stream)
 
 
 def gqa_kv_read_mxfp4(k_out, v_out, k_codes, k_scales, v_codes, v_scales, pos, stream=None) -> None:
@@ -610,10 +606,7 @@ def gqa_kv_read_mxfp4(k_out, v_out, k_codes, k_scales, v_codes, v_scales, pos, s
     assert k_out.shape == (B, T, K, d) and v_out.shape == k_out.shape
     assert k_out.dtype == torch.bfloat16 and v_out.dtype == torch.bfloat16
     assert pos.dtype == torch.int32 and pos.shape == (B,)
-    with _On(stream, k_out, v_out, k_codes, k_scales, v_codes, v_scales, pos) as st:
-        _check("gqa_kv_read_mxfp4",
-               _lib.gqa_kv_read_mxfp4(_ptr(k_out), _ptr(v_out), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
-                                      _ptr(v_scales), _ptr(pos), B, T, K, S_max, d, st))
+    _call("gqa_kv_read_mxfp4", (k_out, v_out, k_codes, k_scales, v_codes, v_scales, pos), (B, T, K, S_max, d), stream)
 
 
 def gqa_decode_mxfp4_workspace_bytes(B: int, H: int, K: int, S_max: int, d: int, num_splits: int = 0) -> int:
@@ -628,8 +621,5 @@ def gqa_decode_mxfp4(out, q, k_codes, k_scales, v_codes, v_scales, seqlens, scal
     assert _mx_shapes(k_codes, k_scales, v_codes, v_scales) == (B, K, S_max, d)
     assert out.shape == q.shape and q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16
     assert seqlens.dtype == torch.int32 and seqlens.shape == (B,)
-    with _On(stream, out, q, k_codes, k_scales, v_codes, v_scales, seqlens, workspace) as st:
-        _check("gqa_decode_mxfp4",
-               _lib.gqa_decode_mxfp4(_ptr(out), _ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
-                                     _ptr(seqlens), B, H, K, S_max, d, float(scale), int(num_splits),
-                                     _ptr(workspace), _ws(workspace), st))
+    _call("gqa_decode_mxfp4", (out, q, k_codes, k_scales, v_codes, v_scales, seqlens, workspace),
+          (B, H, K, S_max, d, float(scale), int(num_splits)), stream, after=())
