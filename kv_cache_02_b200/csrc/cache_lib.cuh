@@ -118,7 +118,7 @@ bool plan_scores(ScoresPlan& sp, int B, int H, int K, int S_max, int d, int num_
   sp.ml_off = sp.pl.nsplit > 1 ? parts * d * sizeof(float) : 0;
   sp.queue_off = (sp.ml_off + parts * sizeof(float2) + 15) / 16 * 16;
   sp.x_off = sp.queue_off + 16;
-  sp.bytes = sp.x_off + (size_t)B * H * S_max * sizeof(float);
+  sp.bytes = sp.x_off + (size_t)B * H * (((size_t)S_max + 3) / 4 * 4) * sizeof(float);
   return true;
 }
 
@@ -193,6 +193,7 @@ int decode_scores_impl(void* out, float* scores, const void* q, const void* k_ca
   gqa::ScoresParams x;
   x.x = reinterpret_cast<float*>(ws + sp.x_off);
   x.scores = scores;
+  x.x_stride = (S_max + 3) / 4 * 4;
   cudaStream_t st = (cudaStream_t)stream;
   const uint64_t rows = pc ? (uint64_t)pc->num_blocks * K * pc->block_size : (uint64_t)B * K * S_max;
   int rc = d == 128 ? launch_scores_decode<128>(sp, p, x, k_cache, v_cache, rows, st)
@@ -410,17 +411,9 @@ int launch_prompt(const PromptPlan& pl, gqa::PromptParams p, const void* q, cons
 // ----------------------------------------------------------------------------
 // gqa_decode_mxfp4
 
-// [rows, 64] bytes of codes, 64-byte swizzle, box of box_rows rows
+// [rows, 64] bytes of codes (rows even) as [rows / 2, 128], 128-byte swizzle, box of box_rows rows
 bool encode_rows_mx(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {gqa::kMxRowBytes, rows};
-  cuuint64_t strides[1] = {gqa::kMxRowBytes};
-  cuuint32_t box[2] = {gqa::kMxRowBytes, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_rows_u8(map, base, rows / 2, box_rows / 2);
 }
 
 struct MxPlan {
@@ -438,7 +431,10 @@ bool plan_mx(MxPlan& pl, int B, int H, int K, int S_max, int d, int num_splits, 
   if (num_splits > 0) {
     splits = std::min(num_splits, max_splits);
   } else {
-    const long long target = 9ll * sms;  // items
+    // two items per resident CTA (8 x 32 x 8 x 128 over 8192 keys: 22.7 us at one, 24.3 at two, 25.3 at three;
+    // one leaves nothing to balance unequal lengths with), four for batches of many units, which are seldom of one
+    // length (32 sequences of 1K to 16K tokens: 71.7 us at four, 78.4 at two)
+    const long long target = (units >= 128 ? 4ll : 2ll) * gqa::kMxCtasPerSm * sms;
     splits = (int)std::max<long long>(1, (target + units - 1) / std::max<long long>(units, 1));
     splits = std::min(splits, std::max(1, (S_max + 511) / 512));
     splits = std::min(splits, max_splits);
@@ -679,7 +675,7 @@ int gqa_decode_mxfp4(void* out, const void* q, const uint8_t* k_codes, const uin
     configured[dev].store(1, std::memory_order_release);
   }
   cudaStream_t st = (cudaStream_t)stream;
-  const int rc = gqa::launch_kernel(gqa::decode_mxfp4_kernel, (unsigned)pl.grid, gqa::kDecThreads,
+  const int rc = gqa::launch_kernel(gqa::decode_mxfp4_kernel, (unsigned)pl.grid, gqa::kMxDecThreads,
                                     gqa::MxCfg::kSmemBytes, st, true, tk, tv, tk16, tv16, p, mp);
   if (rc != GQA_OK || pl.nsplit == 1) return rc;
   return launch_combine(out, p, seqlens, H, K, S_max, p.G, pl.chunk, pl.nsplit, 1, d, GQA_BF16, pl.nsplit > 32,

@@ -1,7 +1,7 @@
 // gqa_decode_mxfp4: the decode of decode.cuh over the 4-bit cache of mxfp4.cuh.
 //
 // Same work items, ring and split merge. A stage holds 128 keys: K and V
-// codes (64-byte rows, 64-byte swizzle), their scales (a 32-bit word per key
+// codes (64-byte rows), their scales (a 32-bit word per key
 // and tensor) and, with an item's first tile, its q rows. Each of the four
 // consumer warps takes 32 keys, as two independent 16-key blocks.
 //
@@ -13,16 +13,22 @@
 //     held in fp16 over a power of two of its own per head, 2^8 at the top:
 //     exact for elements down to 2^-25 of the head's largest.
 //   O = sum over keys of P (V codes) 2^(E_v - 127): the scale goes with P.
-//     A transposing ldmatrix gives a lane 4 dims of two keys; byte permutes
-//     pair the keys.
+//     A transposing ldmatrix gives a lane 4 dims of keys 2 t and 2 t + 1, and
+//     a second one of 2 t + 8 and 2 t + 9; interleaving the two words' nibbles
+//     makes each byte one dim of two keys (8 apart), which the conversion
+//     turns into a register of the A operand. P^T takes the same key order.
 //
 // P 2^(E_v - 127) leaves fp16's range, so each warp holds a reference exponent
-// R per block and multiplies 2^14 P by 2^(E_v - R + 1). While every E_v of the
+// R per block and multiplies 2^10 P by 2^(E_v - R + 1). While every E_v of the
 // step lies in [R - 15, R] (E_v = R - j costs j bits of the range) that product
-// holds P's 11 bits down to P = 2^(j - 29) and anything of it down to
-// 2^(j - 39). A step outside the range raises R, or when the range itself is
+// holds P's 11 bits down to P = 2^(j - 25) and anything of it down to
+// 2^(j - 35). A step outside the range raises R, or when the range itself is
 // too small takes the same product in bf16, whose exponents need no reference
 // (slower: a further conversion per code).
+//
+// P is relative to a reference score m that follows the running maximum only
+// when a step exceeds it by 2^4: the exchange between lanes that finds the
+// maximum is then a rare step, and P stays below 2^14.
 #pragma once
 
 #include "decode.cuh"
@@ -30,10 +36,14 @@
 
 namespace gqa {
 
-constexpr int kMxTileKeys = 128;
+constexpr int kMxWarps = 4;  // consumers
+constexpr int kMxDecThreads = (kMxWarps + 1) * 32;
 constexpr int kMxWarpKeys = 32;
+constexpr int kMxTileKeys = kMxWarps * kMxWarpKeys;
 constexpr int kMxStages = 3;
 constexpr int kMxCtasPerSm = 3;
+constexpr float kMxLag = 4.f;    // how far scores may pass m
+constexpr float kMxBias = 10.f;  // 2^(x - m + kMxBias + 1) stays below fp16's 65504
 constexpr int kMxSpan = 15;      // E_v of the fp16 product: [R - kMxSpan, R]
 constexpr int kMxHeadroom = 2;   // a raised R lies this far above the step's largest E_v
 
@@ -42,7 +52,7 @@ struct MxCfg {
   static constexpr int kScaleOff = 2 * kCodeBytes;                  // K scales, then V scales
   static constexpr int kQOff = kScaleOff + 2 * kMxTileKeys * 4;
   static constexpr int kStageBytes = kQOff + kDecHeadsPerCta * kMxD * 2;
-  static constexpr int kMergeFloats = kDecConsumerWarps * (2 * kDecHeadsPerCta + kDecHeadsPerCta * kMxD);
+  static constexpr int kMergeFloats = kMxWarps * (2 * kDecHeadsPerCta + kDecHeadsPerCta * kMxD);
   static constexpr int kMergeOff = kMxStages * kStageBytes;
   static constexpr int kInfoOff = kMergeOff + kMergeFloats * 4;
   static constexpr int kBarOff = kInfoOff + kMxStages * 16;
@@ -54,19 +64,12 @@ struct MxParams {
   const uint8_t *k_scales, *v_scales;
 };
 
-// Byte offset of 16-byte chunk `chunk` (0..3) of row `row` of 64-byte rows
-// written by TMA with CU_TENSOR_MAP_SWIZZLE_64B.
-__device__ __forceinline__ uint32_t sw64(uint32_t row, uint32_t chunk) {
-  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
-}
-
-// 8 codes of a word -> 4 f16x2: r[i] = (code 2 i, code 2 i + 1)
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
-  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
-      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
-      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w));
+// Byte offset of 16-byte chunk `chunk` (0..3) of key `key` of a tile of codes:
+// TMA writes two keys as one 128-byte row, 128-byte swizzled (64-byte rows
+// would be twice as many rows for TMA; eight consecutive keys' chunks lie in
+// eight different bank groups either way).
+__device__ __forceinline__ uint32_t mx_at(uint32_t key, uint32_t chunk) {
+  return sw128(key >> 1, (key & 1u) * 4u + chunk);
 }
 
 // Four scale bytes -> their values 2^(E - 127) (NaN for 255), by way of bf16, which holds every one of them.
@@ -98,20 +101,22 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return c;
 }
 
-__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t c;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(c) : "r"(a), "r"(b), "r"(sel));
   return c;
 }
 
-// f16x2 -> bf16x2; the e2m1 values are exact in both
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return pack_bf16x2(f.x, f.y);
+// The low (even) and the high (odd) nibbles of a's and b's bytes, a's in the low halves
+__device__ __forceinline__ uint32_t even_nibbles(uint32_t a, uint32_t b) {
+  return (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+}
+__device__ __forceinline__ uint32_t odd_nibbles(uint32_t a, uint32_t b) {
+  return ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
 }
 
-// Running state of one consumer warp. l is held times 2^14, o times 2^15 and
-// over 2^(R - 127) of its 32-dim block; m is the running maximum of the scores.
+// Running state of one consumer warp. l is held times 2^kMxBias, o times twice
+// that and over 2^(R - 127) of its 32-dim block; m is the scores' reference.
 struct MxState {
   float m_a, m_b, l_a, l_b;
   uint32_t ref;  // R of block i in byte i, 16 or more; the same in all lanes
@@ -214,7 +219,7 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint32_t r[4];
-      ldmatrix_x4(k_base + sw64(row + 16 * nb, 2 * j + ch), r[0], r[1], r[2], r[3]);
+      ldmatrix_x4(k_base + mx_at(row + 16 * nb, 2 * j + ch), r[0], r[1], r[2], r[3]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int b = 2 * j + i;
@@ -244,13 +249,13 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
 
   float mx_a = fmaxf(fmaxf(xa[0], xa[1]), fmaxf(xa[2], xa[3]));
   float mx_b = fmaxf(fmaxf(xb[0], xb[1]), fmaxf(xb[2], xb[3]));
+  if (__any_sync(0xffffffffu, mx_a > st.m_a + kMxLag || mx_b > st.m_b + kMxLag)) {
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) {
-    mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
-    mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
-  }
-  const float mn_a = fmaxf(st.m_a, mx_a), mn_b = fmaxf(st.m_b, mx_b);
-  if (__any_sync(0xffffffffu, mn_a != st.m_a || mn_b != st.m_b)) {
+    for (int off = 4; off < 32; off <<= 1) {
+      mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
+      mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
+    }
+    const float mn_a = fmaxf(st.m_a, mx_a), mn_b = fmaxf(st.m_b, mx_b);
     const float al_a = fast_exp2(st.m_a - mn_a), al_b = fast_exp2(st.m_b - mn_b);
     st.m_a = mn_a;
     st.m_b = mn_b;
@@ -265,7 +270,7 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
     }
   }
   float pa[4], pb[4];
-  const float r_a = mn_a - 14.f, r_b = mn_b - 14.f;
+  const float r_a = st.m_a - kMxBias, r_b = st.m_b - kMxBias;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     pa[i] = fast_exp2(xa[i] - r_a);
@@ -301,96 +306,79 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
     const uint32_t base4 = (ref - 0x10101010u) << 2;
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb) {
-      uint32_t pt[2], e0[2], e1[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        pt[i] = movmatrix_trans(pack_f16x2(pa[2 * nb + i], pb[2 * nb + i]));
-        e0[i] = ev[2 * nb + i].x * 4u - base4;
-        e1[i] = ev[2 * nb + i].y * 4u - base4;
-      }
+      const uint32_t p0 = movmatrix_trans(pack_f16x2(pa[2 * nb], pb[2 * nb]));
+      const uint32_t p1 = movmatrix_trans(pack_f16x2(pa[2 * nb + 1], pb[2 * nb + 1]));
+      const uint32_t pe = prmt(p0, p1, 0x5410u), po = prmt(p0, p1, 0x7632u);  // keys (2 t, 2 t + 8), (2 t + 1, 2 t + 9)
+      const uint32_t e00 = ev[2 * nb].x * 4u - base4, e01 = ev[2 * nb].y * 4u - base4;
+      const uint32_t e80 = ev[2 * nb + 1].x * 4u - base4, e81 = ev[2 * nb + 1].y * 4u - base4;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t r[4];
-        ldmatrix_x4_trans(v_base + sw64(row + 16 * nb, 2 * j + ch), r[0], r[1], r[2], r[3]);
+        ldmatrix_x4_trans(v_base + mx_at(row + 16 * nb, 2 * j + ch), r[0], r[1], r[2], r[3]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int b = 2 * j + i;
-          constexpr uint32_t kSel[4] = {0x4000u, 0x5010u, 0x6020u, 0x7030u};
-          const uint32_t q0 = hmul2(pt[0], __byte_perm(e0[0], e1[0], kSel[b]) & 0xff00ff00u);
-          const uint32_t q1 = hmul2(pt[1], __byte_perm(e0[1], e1[1], kSel[b]) & 0xff00ff00u);
-          uint32_t lo[4], hi[4];  // keys 2t, 2t + 1: (k0 d0 d1) (k0 d2 d3) (k1 d0 d1) (k1 d2 d3)
-          e2m1x8_to_f16(r[2 * i], lo);
-          e2m1x8_to_f16(r[2 * i + 1], hi);
-          mma_f16_16816(st.o[2 * b], __byte_perm(lo[0], lo[2], 0x5410), __byte_perm(lo[0], lo[2], 0x7632),
-                        __byte_perm(hi[0], hi[2], 0x5410), __byte_perm(hi[0], hi[2], 0x7632), q0, q1);
-          mma_f16_16816(st.o[2 * b + 1], __byte_perm(lo[1], lo[3], 0x5410), __byte_perm(lo[1], lo[3], 0x7632),
-                        __byte_perm(hi[1], hi[3], 0x5410), __byte_perm(hi[1], hi[3], 0x7632), q0, q1);
+          // byte b of both words in the halves' high bytes; the low ones: a sign, 0
+          constexpr uint32_t kSel[4] = {0x4808u, 0x5818u, 0x6828u, 0x7838u};
+          const uint32_t q0 = hmul2(pe, prmt(e00, e80, kSel[b]));
+          const uint32_t q1 = hmul2(po, prmt(e01, e81, kSel[b]));
+          uint32_t ce[4], co[4];  // dims 0, 2 and 1, 3 of keys (2 t, 2 t + 8), then of (2 t + 1, 2 t + 9)
+          e2m1x8_to_f16(even_nibbles(r[2 * i], r[2 * i + 1]), ce);
+          e2m1x8_to_f16(odd_nibbles(r[2 * i], r[2 * i + 1]), co);
+          mma_f16_16816(st.o[2 * b], ce[0], co[0], ce[2], co[2], q0, q1);
+          mma_f16_16816(st.o[2 * b + 1], ce[1], co[1], ce[3], co[3], q0, q1);
         }
       }
     }
   } else {
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb) {
-      uint32_t pt[2];
+      const uint32_t p0 = movmatrix_trans(pack_bf16x2(pa[2 * nb], pb[2 * nb]));
+      const uint32_t p1 = movmatrix_trans(pack_bf16x2(pa[2 * nb + 1], pb[2 * nb + 1]));
+      const uint32_t pe = prmt(p0, p1, 0x5410u), po = prmt(p0, p1, 0x7632u);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) pt[i] = movmatrix_trans(pack_bf16x2(pa[2 * nb + i], pb[2 * nb + i]));
-#pragma unroll 1
       for (int j = 0; j < 2; ++j) {
         uint32_t r[4];
-        ldmatrix_x4_trans(v_base + sw64(row + 16 * nb, 2 * j + ch), r[0], r[1], r[2], r[3]);
+        ldmatrix_x4_trans(v_base + mx_at(row + 16 * nb, 2 * j + ch), r[0], r[1], r[2], r[3]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int sh = 8 * (2 * j + i);
+          const int b = 2 * j + i, sh = 8 * b;
           const uint32_t rb = (ref >> sh) & 255u;
-          uint32_t q[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint2 e = ev[2 * nb + u];
-            q[u] = bmul2(pt[u], mx_bf16_scale((e.x >> sh) & 255u, rb) | (mx_bf16_scale((e.y >> sh) & 255u, rb) << 16));
-          }
-          uint32_t lo[4], hi[4];
-          e2m1x8_to_f16(r[2 * i], lo);
-          e2m1x8_to_f16(r[2 * i + 1], hi);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            lo[u] = f16x2_to_bf16x2(lo[u]);
-            hi[u] = f16x2_to_bf16x2(hi[u]);
-          }
-          float acc[2][4];
+          const uint2 e0 = ev[2 * nb], e8 = ev[2 * nb + 1];
+          const uint32_t q0 =
+              bmul2(pe, mx_bf16_scale((e0.x >> sh) & 255u, rb) | (mx_bf16_scale((e8.x >> sh) & 255u, rb) << 16));
+          const uint32_t q1 =
+              bmul2(po, mx_bf16_scale((e0.y >> sh) & 255u, rb) | (mx_bf16_scale((e8.y >> sh) & 255u, rb) << 16));
+          uint32_t ce[4], co[4];
+          e2m1x8_to_f16(even_nibbles(r[2 * i], r[2 * i + 1]), ce);
+          e2m1x8_to_f16(odd_nibbles(r[2 * i], r[2 * i + 1]), co);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            acc[0][u] = j == 0 ? st.o[2 * i][u] : st.o[4 + 2 * i][u];
-            acc[1][u] = j == 0 ? st.o[2 * i + 1][u] : st.o[5 + 2 * i][u];
+            ce[u] = f16x2_to_bf16x2(ce[u]);
+            co[u] = f16x2_to_bf16x2(co[u]);
           }
-          mma_bf16_16816(acc[0], __byte_perm(lo[0], lo[2], 0x5410), __byte_perm(lo[0], lo[2], 0x7632),
-                         __byte_perm(hi[0], hi[2], 0x5410), __byte_perm(hi[0], hi[2], 0x7632), q[0], q[1]);
-          mma_bf16_16816(acc[1], __byte_perm(lo[1], lo[3], 0x5410), __byte_perm(lo[1], lo[3], 0x7632),
-                         __byte_perm(hi[1], hi[3], 0x5410), __byte_perm(hi[1], hi[3], 0x7632), q[0], q[1]);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (j == 0) {
-              st.o[2 * i][u] = acc[0][u];
-              st.o[2 * i + 1][u] = acc[1][u];
-            } else {
-              st.o[4 + 2 * i][u] = acc[0][u];
-              st.o[5 + 2 * i][u] = acc[1][u];
-            }
-          }
+          mma_bf16_16816(st.o[2 * b], ce[0], co[0], ce[2], co[2], q0, q1);
+          mma_bf16_16816(st.o[2 * b + 1], ce[1], co[1], ce[3], co[3], q0, q1);
         }
       }
     }
   }
 }
 
-// End of a work item: the four warps' states merged, then the output (the
+__device__ __forceinline__ void mx_consumer_bar() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kMxWarps * 32) : "memory");
+}
+
+// End of a work item: the warps' states merged, then the output (the
 // unit's only split) or the split's partial.
 __device__ __forceinline__ void mx_epilogue(const DecodeParams& p, const ItemCoord& c, const MxState& st, float* merge,
                                             bool single, int tid, int warp, int lane) {
   constexpr int D = kMxD;
   float* red_m = merge;
-  float* red_l = red_m + kDecConsumerWarps * kDecHeadsPerCta;
-  float* ow = red_l + kDecConsumerWarps * kDecHeadsPerCta + warp * kDecHeadsPerCta * D;
-  consumer_bar();  // the previous item's scratch has been read
+  float* red_l = red_m + kMxWarps * kDecHeadsPerCta;
+  float* red_o = red_l + kMxWarps * kDecHeadsPerCta;
+  float* ow = red_o + warp * kDecHeadsPerCta * D;
+  mx_consumer_bar();  // the previous item's scratch has been read
   float l_a = st.l_a, l_b = st.l_b;
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
@@ -413,23 +401,38 @@ __device__ __forceinline__ void mx_epilogue(const DecodeParams& p, const ItemCoo
     *reinterpret_cast<float4*>(ow + ha * D + dim) = make_float4(o0[0] * f, o0[2] * f, o1[0] * f, o1[2] * f);
     *reinterpret_cast<float4*>(ow + (ha + 1) * D + dim) = make_float4(o0[1] * f, o0[3] * f, o1[1] * f, o1[3] * f);
   }
-  consumer_bar();
+  mx_consumer_bar();
   __nv_bfloat16* out_row = static_cast<__nv_bfloat16*>(p.out) + ((size_t)c.b * p.H + c.h0) * D;
   const size_t part = ((size_t)c.unit * p.nsplit + c.split) * p.G + (size_t)c.hsl * kDecHeadsPerCta;
-  for (int i = tid; i < c.nh * D; i += kDecConsumerWarps * 32) {
-    const int h = i / D, dim = i % D;
-    float M, L, O;
-    merged<D>(merge, h, dim, M, L, O);
+  // four dims a thread
+  for (int i = tid; i < c.nh * (D / 4); i += kMxWarps * 32) {
+    const int h = i / (D / 4), dim = i % (D / 4) * 4;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kMxWarps; ++w) M = fmaxf(M, red_m[w * 8 + h]);
+    float L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kMxWarps; ++w) {
+      const float f = fast_exp2(red_m[w * 8 + h] - M);
+      const float4 v = *reinterpret_cast<const float4*>(red_o + (w * kDecHeadsPerCta + h) * D + dim);
+      L = fmaf(red_l[w * 8 + h], f, L);
+      O.x = fmaf(v.x, f, O.x);
+      O.y = fmaf(v.y, f, O.y);
+      O.z = fmaf(v.z, f, O.z);
+      O.w = fmaf(v.w, f, O.w);
+    }
     if (single) {
-      out_row[i] = __float2bfloat16_rn(O / L);
+      *reinterpret_cast<uint2*>(out_row + h * D + dim) =
+          make_uint2(pack_bf16x2(O.x / L, O.y / L), pack_bf16x2(O.z / L, O.w / L));
     } else {
-      p.ws_o[(part + h) * D + dim] = O;
+      *reinterpret_cast<float4*>(p.ws_o + (part + h) * D + dim) = O;
       if (dim == 0) p.ws_ml[part + h] = make_float2(M, L);
     }
   }
 }
 
-__global__ void __launch_bounds__(kDecThreads, kMxCtasPerSm)
+__global__ void __launch_bounds__(kMxDecThreads, kMxCtasPerSm)
     decode_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
                         const DecodeParams p, const MxParams mp) {
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kDecThreads, kMxCtasPerSm)
   // before the grid dependency, as in decode_bf16_kernel: barriers, descriptors, an L2 warm-up (a hint) of the
   // first work item's codes, sized by a length that may be stale
   int spec_first = 0;
-  if (warp == kDecConsumerWarps && lane == 0) {
+  if (warp == kMxWarps && lane == 0) {
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
     prefetch_tensormap(&tm_k16);
@@ -459,17 +462,17 @@ __global__ void __launch_bounds__(kDecThreads, kMxCtasPerSm)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMxStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kDecConsumerWarps);
+      mbar_init(&empty[s], kMxWarps);
     }
     fence_mbar_init();
   }
   __syncthreads();
-  if (warp == kDecConsumerWarps && lane == 0 && (int)blockIdx.x < p.nitems)
+  if (warp == kMxWarps && lane == 0 && (int)blockIdx.x < p.nitems)
     warm_first_item<kMxRowBytes>(p, item_coord(p, blockIdx.x), spec_first, kMxStages * kMxTileKeys);
   grid_dep_wait();
   grid_dep_launch();
 
-  if (warp == kDecConsumerWarps) {
+  if (warp == kMxWarps) {
     if (lane != 0) return;
     const uint64_t policy = l2_policy_evict_first();
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
@@ -509,15 +512,15 @@ __global__ void __launch_bounds__(kDecThreads, kMxCtasPerSm)
         const int row0 = c.unit * p.S_max + t0;
         if (rows == kMxTileKeys) {
           mbar_arrive_expect_tx(&full[s], 2u * C::kCodeBytes + 2u * sbytes + q_bytes);
-          tma_load_2d(stage, &tm_k, 0, row0, &full[s], policy);
-          tma_load_2d(stage + C::kCodeBytes, &tm_v, 0, row0, &full[s], policy);
+          tma_load_2d(stage, &tm_k, 0, row0 / 2, &full[s], policy);
+          tma_load_2d(stage + C::kCodeBytes, &tm_v, 0, row0 / 2, &full[s], policy);
         } else {
           const int nbox = (rows + kDecBoxRows - 1) / kDecBoxRows;
           mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * nbox * kDecBoxRows * kMxRowBytes) + 2u * sbytes + q_bytes);
           for (int bx = 0; bx < nbox; ++bx) {
             const int off = bx * kDecBoxRows * kMxRowBytes;
-            tma_load_2d(stage + off, &tm_k16, 0, row0 + bx * kDecBoxRows, &full[s], policy);
-            tma_load_2d(stage + C::kCodeBytes + off, &tm_v16, 0, row0 + bx * kDecBoxRows, &full[s], policy);
+            tma_load_2d(stage + off, &tm_k16, 0, (row0 + bx * kDecBoxRows) / 2, &full[s], policy);
+            tma_load_2d(stage + C::kCodeBytes + off, &tm_v16, 0, (row0 + bx * kDecBoxRows) / 2, &full[s], policy);
           }
         }
         bulk_load(stage + C::kScaleOff, mp.k_scales + (size_t)row0 * kMxScales, sbytes, &full[s]);

@@ -17,8 +17,9 @@
 namespace gqa {
 
 struct ScoresParams {
-  float* x;       // [B * H, S_max] scaled scores
+  float* x;       // [B * H, x_stride] scaled scores
   float* scores;  // [B, K, S_max]
+  int x_stride;   // S_max rounded up to 4
 };
 
 // warp_tile of decode.cuh, storing the scaled scores of the warp's keys: xa, xb
@@ -254,9 +255,9 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     }
     if (kb < si.rows) {
       const int h = 2 * (lane & 3);
-      float* x = sp.x + ((size_t)cur.b * p.H + cur.h0 + h) * p.S_max + t0 + kb;
+      float* x = sp.x + ((size_t)cur.b * p.H + cur.h0 + h) * sp.x_stride + t0 + kb;
       warp_tile_scores<D>(st, qf, smem_u32(smem + s * C::kStageBytes), kb, si.rows, lane, p.scale_log2,
-                          h < cur.nh ? x : nullptr, h + 1 < cur.nh ? x + p.S_max : nullptr);
+                          h < cur.nh ? x : nullptr, h + 1 < cur.nh ? x + sp.x_stride : nullptr);
     }
     t0 += kDecTileKeys;
     __syncwarp();
@@ -267,8 +268,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 }
 
 // The join. A CTA takes kAccKeys rows of one unit. Its warps first join the
-// splits' (m, l) of the group's heads; then a thread per row adds up the
-// heads' weights in order, and the unit's output columns are shared out among
+// splits' (m, l) of the group's heads; then a thread adds up the heads'
+// weights of four rows, in order of the heads, and the unit's output columns are shared out among
 // the unit's CTAs, a CTA's threads over the splits of its columns (summed in
 // a fixed order).
 constexpr int kAccThreads = 256;
@@ -277,11 +278,11 @@ constexpr int kAccHeads = 64;  // heads whose (M, 1 / L) are held at a time
 constexpr int kAccBatch = 8;   // heads whose scores a thread asks for at once
 
 template <int D>
-__global__ void __launch_bounds__(kAccThreads)
+__global__ void __launch_bounds__(kAccThreads, 4)
     scores_finish_kernel(const DecodeParams p, const ScoresParams sp, int chunks) {
   __shared__ float2 ml[kAccHeads];
   __shared__ float4 red[kAccThreads];
-  constexpr int J = kAccKeys / kAccThreads;
+  static_assert(kAccKeys == 4 * kAccThreads, "four rows a thread");
   const int unit = blockIdx.x / chunks, part = blockIdx.x % chunks;
   const int b = unit / p.K, g = unit % p.K;
   const int k0 = part * kAccKeys;
@@ -295,21 +296,16 @@ __global__ void __launch_bounds__(kAccThreads)
   const int active = (len + kAccKeys - 1) / kAccKeys;  // CTAs of the unit that have rows
   // the output columns of this CTA, four dims each
   const int cols = p.G * (D / 4), per = (cols + active - 1) / active;
-  const float* x0 = sp.x + ((size_t)b * p.H + (size_t)g * p.G) * p.S_max + k0 + tid;
-  float acc[J];
-#pragma unroll
-  for (int j = 0; j < J; ++j) acc[j] = 0.f;
+  const float* x0 = sp.x + ((size_t)b * p.H + (size_t)g * p.G) * sp.x_stride + k0 + 4 * tid;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int h0 = 0; h0 < p.G; h0 += kAccHeads) {
     const int nh = min(kAccHeads, p.G - h0);
-    float x[kAccBatch][J];
-    auto ask = [&](int h) {
+    float4 x[kAccBatch];
+    auto ask = [&](int h) {  // rows from n on hold anything: their sums are not used
 #pragma unroll
       for (int i = 0; i < kAccBatch; ++i)
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-          x[i][j] = h + i < nh && tid + j * kAccThreads < n
-                        ? __ldcg(x0 + (size_t)(h0 + h + i) * p.S_max + j * kAccThreads)
-                        : -INFINITY;
+        if (h + i < nh && 4 * tid < n)
+          x[i] = __ldcg(reinterpret_cast<const float4*>(x0 + (size_t)(h0 + h + i) * sp.x_stride));
     };
     ask(0);
     if (h0 > 0) __syncthreads();
@@ -338,8 +334,10 @@ __global__ void __launch_bounds__(kAccThreads)
       for (int i = 0; i < kAccBatch; ++i) {
         if (h + i < nh) {
           const float2 z = ml[h + i];
-#pragma unroll
-          for (int j = 0; j < J; ++j) acc[j] = fmaf(fast_exp2(x[i][j] - z.x), z.y, acc[j]);
+          acc.x = fmaf(fast_exp2(x[i].x - z.x), z.y, acc.x);
+          acc.y = fmaf(fast_exp2(x[i].y - z.x), z.y, acc.y);
+          acc.z = fmaf(fast_exp2(x[i].z - z.x), z.y, acc.z);
+          acc.w = fmaf(fast_exp2(x[i].w - z.x), z.y, acc.w);
         }
       }
     }
@@ -368,11 +366,19 @@ __global__ void __launch_bounds__(kAccThreads)
             o.w = fmaf(v.w, f, o.w);
           }
         }
+        // the slots of a column: over the lanes of a warp, then over warps
+        for (int off = 16; off >= width; off >>= 1) {
+          o.x += __shfl_xor_sync(0xffffffffu, o.x, off);
+          o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
+          o.z += __shfl_xor_sync(0xffffffffu, o.z, off);
+          o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
+        }
         red[tid] = o;
         __syncthreads();
         if (slot == 0 && col < c1) {
-          for (int s = 1; s < slots; ++s) {
-            const float4 v = red[s * width + cc];
+          const int step = max(width, 32);
+          for (int t = tid + step; t < kAccThreads; t += step) {
+            const float4 v = red[t];
             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
           }
           const float inv = ml[h - h0].y;
@@ -383,10 +389,17 @@ __global__ void __launch_bounds__(kAccThreads)
       }
     }
   }
+  float* dst = sp.scores + (size_t)unit * p.S_max + k0 + 4 * tid;
+  const int left = n - 4 * tid;
+  if (left >= 4 && (p.S_max & 3) == 0) {
+    float4 v = *reinterpret_cast<const float4*>(dst);
+    v.x += acc.x, v.y += acc.y, v.z += acc.z, v.w += acc.w;
+    *reinterpret_cast<float4*>(dst) = v;
+  } else {
+    const float a[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int i = tid + j * kAccThreads;
-    if (i < n) sp.scores[(size_t)unit * p.S_max + k0 + i] += acc[j];
+    for (int j = 0; j < 4; ++j)
+      if (j < left) dst[j] += a[j];
   }
 }
 

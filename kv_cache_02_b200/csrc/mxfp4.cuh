@@ -35,9 +35,37 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
   return r;
 }
 
-// The value of exponent E: 2^(E - 127), NaN for 255
-__device__ __forceinline__ float e8m0_value(uint32_t e) {
-  return e == 0 ? __uint_as_float(0x00400000u) : e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(e << 23);
+// Maxima of the two unsigned halves
+__device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
+// 8 codes of a word -> 4 f16x2: r[i] = (code 2 i, code 2 i + 1)
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
+// f16x2 -> bf16x2; the e2m1 values are exact in both
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_bf16x2(f.x, f.y);
+}
+
+// The value of exponent E, 2^(E - 127), NaN for 255, in both halves as bfloat16
+__device__ __forceinline__ uint32_t e8m0_bf16x2(uint32_t e) {
+  return (e == 0 ? 0x0040u : e == 255 ? 0x7fc0u : e << 7) * 0x10001u;
 }
 
 constexpr int kMxLanes = 8;    // lanes of a row
@@ -78,21 +106,23 @@ __global__ void __launch_bounds__(kMxThreads)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t u[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
-        uint32_t top = 0;  // the block's largest magnitude, as bits: a NaN's are above infinity's
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max((u[j] << 16) & 0x7fffffffu, u[j] & 0x7fff0000u));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const bool bad = top >= 0x7f800000u;
-        e[h] = bad ? 255u : (uint32_t)max((int)(top >> 23) - 2, 0);
-        const float inv = bad ? 0.f : __uint_as_float((254u - e[h]) << 23);  // 2^(127 - E), exact
+        // the block's largest magnitude, as bits: a NaN's are above infinity's
+        uint32_t top = umax2(umax2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu), umax2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
+        top = umax2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = umax2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = max(top & 0xffffu, top >> 16);
+        const bool bad = top >= 0x7f80u;
+        e[h] = bad ? 255u : (uint32_t)max((int)(top >> 7) - 2, 0);
+        // times 2^(127 - E), in bfloat16: exact, but for values far below a quarter of the scale
+        const uint32_t inv = bad ? 0u : ((254u - e[h]) << 7) * 0x10001u;
         float x[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x[2 * j] = bad ? 0.f : __uint_as_float(u[j] << 16) * inv;
-          x[2 * j + 1] = bad ? 0.f : __uint_as_float(u[j] & 0xffff0000u) * inv;
+          const uint32_t v = bmul2(u[j], inv);
+          x[2 * j] = __uint_as_float(v << 16);
+          x[2 * j + 1] = __uint_as_float(v & 0xffff0000u);
         }
-        codes[h] = e2m1x8(x);
+        codes[h] = bad ? 0u : e2m1x8(x);
       }
       // the row's four scales in lane 0: blocks 0, 2 are its own, 1, 3 those of lane 4
       uint32_t sc = e[0] | (e[1] << 16);
@@ -109,22 +139,12 @@ __global__ void __launch_bounds__(kMxThreads)
   }
 }
 
-// 8 e2m1 codes times the scale -> bf16 values, exact
-__device__ __forceinline__ uint4 mx_values8(uint32_t codes, float scale) {
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float v[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t c = codes >> (8 * i + 4 * j);
-      // the code's exponent and mantissa bits at the top of an fp16 one: value * 2^-14
-      const uint32_t h = ((c & 7u) << 9) | ((c & 8u) << 12);
-      v[j] = __half2float(__ushort_as_half((unsigned short)h)) * 16384.f * scale;
-    }
-    out[i] = pack_bf16x2(v[0], v[1]);
-  }
-  return make_uint4(out[0], out[1], out[2], out[3]);
+// 8 e2m1 codes times the scale -> bf16 values (one rounding, of results past bfloat16's ends alone)
+__device__ __forceinline__ uint4 mx_values8(uint32_t codes, uint32_t scale) {
+  uint32_t h[4];
+  e2m1x8_to_f16(codes, h);
+  return make_uint4(bmul2(f16x2_to_bf16x2(h[0]), scale), bmul2(f16x2_to_bf16x2(h[1]), scale),
+                    bmul2(f16x2_to_bf16x2(h[2]), scale), bmul2(f16x2_to_bf16x2(h[3]), scale));
 }
 
 __global__ void __launch_bounds__(kMxThreads)
@@ -164,8 +184,8 @@ __global__ void __launch_bounds__(kMxThreads)
       const unsigned r = r0 + i * (kMxThreads / kMxLanes);
       if (r >= nrows) continue;
       const uint32_t mine = sc[i] >> (8 * (l >> 2));  // blocks l / 4 and l / 4 + 2
-      out[(size_t)r * 16] = mx_values8(codes[i][0], e8m0_value(mine & 255u));
-      out[(size_t)r * 16 + 8] = mx_values8(codes[i][1], e8m0_value((mine >> 16) & 255u));
+      out[(size_t)r * 16] = mx_values8(codes[i][0], e8m0_bf16x2(mine & 255u));
+      out[(size_t)r * 16 + 8] = mx_values8(codes[i][1], e8m0_bf16x2((mine >> 16) & 255u));
     }
   }
 }

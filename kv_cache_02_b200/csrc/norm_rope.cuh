@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
   const int l = threadIdx.x % LPR;
   const bool live = group < (unsigned)(p.B * p.T) * (unsigned)p.chunks;
   const unsigned n = live ? group / (unsigned)p.chunks : 0u;
-  const int chunk = live ? (int)(group - n * (unsigned)p.chunks) : nrows;  // rows chunk, chunk + chunks, ...
+  const int chunk = live ? (int)(group - n * (unsigned)p.chunks) : nrows;  // rows R chunk, R chunk + 1, ...
 
   // the lane's two chunks of a row, and whether they are rotated (all 8 values or none)
   const int rd = p.rotary_dim;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
   Raw w[R][2];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int row = chunk + r * p.chunks;
+    const int row = R * chunk + r;
     w[r][0] = w[r][1] = Q::zero();
     if (row < nrows) {
       const T* x = (row < p.H ? q : row < p.H + p.K ? k : v) + row * D;
@@ -162,11 +162,13 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
     *reinterpret_cast<Raw*>(dst + lo) = y[0];
     *reinterpret_cast<Raw*>(dst + hi) = y[1];
   };
+  const T* wt = nullptr;
+  float wv[8];
   T* q_out = static_cast<T*>(p.q_out) + (long long)n * p.H * D;
   T* k_out = p.k_out ? static_cast<T*>(p.k_out) + (long long)n * p.K * D : nullptr;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int row = chunk + r * p.chunks;
+    const int row = R * chunk + r;
     const bool is_q = row < p.H, is_k = !is_q && row < p.H + p.K;
     float x[8];
     Q::unpack(w[r][0], x);
@@ -176,12 +178,15 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
     for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
     for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off, LPR);
-    const T* wt = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+    if (r == 0 || row == p.H) {
+      wt = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+      if (wt != nullptr) {
+        Q::unpack(__ldg(reinterpret_cast<const Raw*>(wt + lo)), wv);
+        Q::unpack(__ldg(reinterpret_cast<const Raw*>(wt + hi)), wv + 4);
+      }
+    }
     if (wt != nullptr) {
-      const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-      float wv[8];
-      Q::unpack(__ldg(reinterpret_cast<const Raw*>(wt + lo)), wv);
-      Q::unpack(__ldg(reinterpret_cast<const Raw*>(wt + hi)), wv + 4);
+      const float inv = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * wv[i];
     }
