@@ -328,7 +328,7 @@ int launch_mx_rows(void (*kernel)(KArgs...), int B, int T, int K, cudaStream_t s
 struct PromptPlan {
   int tile_tokens = 0, n_rt = 0, n_kt = 0;
   int key_splits = 1, row_splits = 1;  // of the kRows and the kKeys kernel
-  size_t ml_off = 0, part_off = 0, bytes = 0;
+  size_t ml_off = 0, part_off = 0, queue_off = 0, bytes = 0;
 };
 
 bool plan_prompt(PromptPlan& pl, int B, int T, int H, int K, int S_max, int d, int sms) {
@@ -338,19 +338,24 @@ bool plan_prompt(PromptPlan& pl, int B, int T, int H, int K, int S_max, int d, i
   pl.n_rt = (T + pl.tile_tokens - 1) / pl.tile_tokens;
   pl.n_kt = (S_max + gqa::kPsRows - 1) / gqa::kPsRows;
   const long long units = (long long)B * K;
-  // four items per SM (two CTAs are resident), four streamed tiles in each
+  // about two items (pairs of stationary tiles) per SM, four streamed tiles in each
   auto splits = [&](int tiles, int streamed) {
-    const long long items = units * std::max(tiles, 1);
-    const long long want = (4ll * sms + items - 1) / std::max(items, 1ll);
+    const long long items = units * std::max((tiles + 1) / 2, 1);
+    const long long want = (2ll * sms + items - 1) / std::max(items, 1ll);
     return (int)std::max(1ll, std::min<long long>(want, streamed / 4));
   };
   pl.key_splits = splits(pl.n_rt, pl.n_kt);
   pl.row_splits = splits(pl.n_kt, pl.n_rt);
-  if (units * pl.n_rt * pl.key_splits >= (1ll << 31) || units * pl.n_kt * pl.row_splits >= (1ll << 31)) return false;
+  // below the work counter's range
+  if (units * ((pl.n_rt + 1) / 2) * pl.key_splits + sms >= (1ll << gqa::kCntBits) ||
+      units * ((pl.n_kt + 1) / 2) * pl.row_splits + sms >= (1ll << gqa::kCntBits))
+    return false;
   const size_t rows = (size_t)units * pl.n_rt * gqa::kPsRows;
   pl.ml_off = rows * sizeof(float);
   pl.part_off = pl.ml_off + (pl.key_splits > 1 ? pl.key_splits * rows * sizeof(float2) : 0);
-  pl.bytes = pl.part_off + (pl.row_splits > 1 ? (size_t)pl.row_splits * units * S_max * sizeof(float) : 0);
+  const size_t part_bytes = pl.row_splits > 1 ? (size_t)pl.row_splits * units * S_max * sizeof(float) : 0;
+  pl.queue_off = (pl.part_off + part_bytes + 15) / 16 * 16;
+  pl.bytes = pl.queue_off + 32;  // a work counter for each of the two kernels
   return true;
 }
 
@@ -389,20 +394,21 @@ int launch_prompt(const PromptPlan& pl, gqa::PromptParams p, const void* q, cons
   const int units = p.B * p.K;
   const int sms = sm_count(dev);
   p.splits = pl.key_splits;
-  int rc = gqa::launch_kernel(gqa::prompt_scores_kernel<D, gqa::kPsKindRows>,
-                              (unsigned)((long long)units * p.n_rt * p.splits), gqa::kPsThreads, C::kSmemBytes, st,
-                              true, tq, tk, p);
+  p.items = units * ((p.n_rt + 1) / 2) * p.splits;
+  int rc = gqa::launch_kernel(gqa::prompt_scores_kernel<D, gqa::kPsKindRows>, (unsigned)std::min(p.items, sms),
+                              gqa::kPsThreads, C::kSmemBytes, st, true, tq, tk, p);
   if (rc != GQA_OK) return rc;
   if (p.splits > 1) {
     const long long rows = (long long)units * p.n_rt * gqa::kPsRows;
-    rc = gqa::launch_kernel(gqa::prompt_lse_kernel, (unsigned)grid_for(rows, 256, sms), 256, 0, st, true, p.lse,
+    rc = gqa::launch_kernel(gqa::prompt_lse_kernel, (unsigned)grid_for(rows, 256, sms), 256, 0, st, true, p.nlse,
                             (const float2*)p.ml, rows, p.splits);
     if (rc != GQA_OK) return rc;
   }
   p.splits = pl.row_splits;
-  rc = gqa::launch_kernel(gqa::prompt_scores_kernel<D, gqa::kPsKindKeys>,
-                          (unsigned)((long long)units * p.n_kt * p.splits), gqa::kPsThreads, C::kSmemBytes, st, true,
-                          tq, tk, p);
+  p.items = units * ((p.n_kt + 1) / 2) * p.splits;
+  p.queue += 2;
+  rc = gqa::launch_kernel(gqa::prompt_scores_kernel<D, gqa::kPsKindKeys>, (unsigned)std::min(p.items, sms),
+                          gqa::kPsThreads, C::kSmemBytes, st, true, tq, tk, p);
   if (rc != GQA_OK || p.splits == 1) return rc;
   return gqa::launch_kernel(gqa::prompt_add_kernel, (unsigned)grid_for((long long)units * p.S_max, 256, sms), 256, 0,
                             st, true, p.scores, (const float*)p.part, p.seqlens, units, p.K, p.S_max, p.splits);
@@ -599,9 +605,11 @@ int gqa_prompt_scores(float* scores, const void* q, const void* k_cache, const i
   char* ws = static_cast<char*>(workspace);
   gqa::PromptParams p{};
   p.scores = scores;
-  p.lse = reinterpret_cast<float*>(ws);
+  p.nlse = reinterpret_cast<float*>(ws);
   p.ml = reinterpret_cast<float2*>(ws + pl.ml_off);
   p.part = reinterpret_cast<float*>(ws + pl.part_off);
+  p.queue = reinterpret_cast<unsigned long long*>(ws + pl.queue_off);
+  p.tag = next_call_tag();
   p.seqlens = seqlens;
   p.B = B;
   p.T = T;
