@@ -206,44 +206,34 @@ int decode_scores_impl(void* out, float* scores, const void* q, const void* k_ca
 // ----------------------------------------------------------------------------
 // gqa_kv_evict
 
-// launch_kernel with thread-block clusters of `cluster` CTAs, as a programmatic dependent.
-template <typename... KArgs, typename... Args>
-int launch_clusters(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, int cluster,
-                    cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const QueryErrorScope scope;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return GQA_OK;
-  scope.clear_own();
-  return GQA_ERR_CUDA;
-}
-
 struct EvictPlan {
-  int cluster = 1, seg_keys = 0, max_moves = 0;
-  size_t bytes = 0;
+  bool cta = false, fused = false;  // evict_cta_kernel; with the moves
+  int seg_keys = 0, max_moves = 0;
+  size_t done_off = 0, bytes = 0;
 };
 
 bool plan_evict(EvictPlan& pl, int B, int K, int S_max, int keep) {
   if (B < 0 || K <= 0 || S_max <= 0 || keep <= 0 || keep > S_max) return false;
-  if ((long long)B * K * gqa::kEvMaxCluster >= (1ll << 31)) return false;
-  // one CTA per (b, g) for bounded caches, eight for long ones
-  pl.cluster = S_max > 8192 ? gqa::kEvMaxCluster : 1;
-  const int seg = ((S_max + pl.cluster - 1) / pl.cluster + 31) / 32 * 32;
-  pl.seg_keys = std::min(seg, gqa::kEvMaxSegKeys);
+  if ((long long)B * K * gqa::kEvCluster >= (1ll << 31)) return false;
   pl.max_moves = std::min(keep, S_max - keep);
-  pl.bytes = (size_t)B * K * (1 + 2 * (size_t)pl.max_moves) * sizeof(int32_t);
+  pl.cta = S_max <= gqa::kEvCtaRows;
+  pl.fused = pl.cta && pl.max_moves <= gqa::kEvFusedMoves;
+  const int seg = ((S_max + gqa::kEvCluster - 1) / gqa::kEvCluster + 31) / 32 * 32;
+  pl.seg_keys = std::min(seg, gqa::kEvMaxSegKeys);
+  pl.done_off = pl.fused ? 0 : ((size_t)B * K * (1 + 2 * (size_t)pl.max_moves) * sizeof(int32_t) + 15) / 16 * 16;
+  pl.bytes = pl.done_off + (pl.fused ? (size_t)std::max(B, 1) * sizeof(unsigned long long) : 0);
   return true;
+}
+
+template <bool kFused>
+int launch_evict_cta(const gqa::EvictParams& p, cudaStream_t st) {
+  auto run = [&](auto kernel) {
+    return gqa::launch_kernel(kernel, (unsigned)(p.B * p.K), gqa::kEvThreads, 0, st, true, p);
+  };
+  if (p.S_max <= gqa::kEvThreads) return run(gqa::evict_cta_kernel<1, kFused>);
+  if (p.S_max <= 2 * gqa::kEvThreads) return run(gqa::evict_cta_kernel<2, kFused>);
+  if (p.S_max <= 4 * gqa::kEvThreads) return run(gqa::evict_cta_kernel<4, kFused>);
+  return run(gqa::evict_cta_kernel<8, kFused>);
 }
 
 int kv_evict_impl(void* k_cache, void* v_cache, float* scores, int32_t* row_pos, int32_t* seqlens,
@@ -267,13 +257,14 @@ int kv_evict_impl(void* k_cache, void* v_cache, float* scores, int32_t* row_pos,
   p.seqlens = seqlens;
   p.recent_from = recent_from;
   p.ws = static_cast<int32_t*>(workspace);
+  p.done = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + pl.done_off);
+  p.tag = next_call_tag();
   p.B = B;
   p.K = K;
   p.S_max = S_max;
   p.keep = keep;
   p.sinks = sinks;
   p.max_moves = pl.max_moves;
-  p.cluster = pl.cluster;
   p.seg_keys = pl.seg_keys;
   p.row_chunks = d * (dtype == GQA_F32 ? 4 : 2) / 16;
   if (pc) {
@@ -283,21 +274,28 @@ int kv_evict_impl(void* k_cache, void* v_cache, float* scores, int32_t* row_pos,
     p.max_blocks = pc->max_blocks;
   }
   const int dev = current_device();
-  static DeviceCache configured{};
-  if (dev >= 0 && dev < kMaxDevices && configured[dev].load(std::memory_order_acquire) == 0) {
-    if (cudaFuncSetAttribute(gqa::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             gqa::kEvStaticBytes + gqa::kEvMaxSegKeys * 4) != cudaSuccess)
-      return GQA_ERR_CUDA;
-    configured[dev].store(1, std::memory_order_release);
-  }
   cudaStream_t st = (cudaStream_t)stream;
-  const int rc = launch_clusters(gqa::evict_select_kernel, (unsigned)(B * K * pl.cluster), gqa::kEvThreads,
-                                 (size_t)gqa::kEvStaticBytes + (size_t)pl.seg_keys * 4, pl.cluster, st, p);
-  if (rc != GQA_OK) return rc;
-  // about four CTAs per SM share the moves
   const int units = B * K;
-  const int per = gqa::kEvMoveThreads / (2 * p.row_chunks) * 4;  // rows a CTA has in flight
-  p.ctas_per_unit = std::max(1, std::min((sm_count(dev) * 4 + units - 1) / units, (pl.max_moves + per - 1) / per));
+  int rc;
+  if (pl.cta) {
+    rc = pl.fused ? launch_evict_cta<true>(p, st) : launch_evict_cta<false>(p, st);
+    if (rc != GQA_OK || pl.fused) return rc;
+  } else {
+    static DeviceCache configured{};
+    if (dev >= 0 && dev < kMaxDevices && configured[dev].load(std::memory_order_acquire) == 0) {
+      if (cudaFuncSetAttribute(gqa::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               gqa::kEvStaticBytes + gqa::kEvMaxSegKeys * 4) != cudaSuccess)
+        return GQA_ERR_CUDA;
+      configured[dev].store(1, std::memory_order_release);
+    }
+    rc = gqa::launch_kernel(gqa::evict_select_kernel, (unsigned)(units * gqa::kEvCluster), gqa::kEvThreads,
+                            (size_t)gqa::kEvStaticBytes + (size_t)pl.seg_keys * 4, st, true, p);
+    if (rc != GQA_OK) return rc;
+  }
+  // as many CTAs as have rows to move, up to four per SM over all units
+  const int per = gqa::kEvMoveThreads / (2 * p.row_chunks) * gqa::kEvFlight;  // rows a CTA has in flight
+  p.ctas_per_unit =
+      std::max(1, std::min((sm_count(dev) * 4 + units - 1) / units, (pl.max_moves + per - 1) / per));
   return gqa::launch_kernel(gqa::evict_move_kernel, (unsigned)(units * p.ctas_per_unit), gqa::kEvMoveThreads, 0, st,
                             true, p);
 }

