@@ -269,13 +269,14 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 
 // The join. A CTA takes kAccKeys rows of one unit. Its warps first join the
 // splits' (m, l) of the group's heads; then a thread adds up the heads'
-// weights of four rows, in order of the heads, and the unit's output columns are shared out among
-// the unit's CTAs, a CTA's threads over the splits of its columns (summed in
-// a fixed order).
+// weights of four rows, in order of the heads, and the unit's output columns
+// are shared out among the unit's CTAs, a CTA's threads over the splits of its
+// columns (summed in a fixed order). Latency bounds it: all that does not
+// depend on (m, l) is asked for first.
 constexpr int kAccThreads = 256;
 constexpr int kAccKeys = 1024;
 constexpr int kAccHeads = 64;  // heads whose (M, 1 / L) are held at a time
-constexpr int kAccBatch = 8;   // heads whose scores a thread asks for at once
+constexpr int kAccBatch = 4;   // heads whose scores a thread asks for at once
 
 template <int D>
 __global__ void __launch_bounds__(kAccThreads, 4)
@@ -297,20 +298,35 @@ __global__ void __launch_bounds__(kAccThreads, 4)
   // the output columns of this CTA, four dims each
   const int cols = p.G * (D / 4), per = (cols + active - 1) / active;
   const float* x0 = sp.x + ((size_t)b * p.H + (size_t)g * p.G) * sp.x_stride + k0 + 4 * tid;
+  const float2* unit_ml = p.ws_ml + (size_t)unit * p.nsplit * p.G;
+  const float4* unit_o = reinterpret_cast<const float4*>(p.ws_o + (size_t)unit * p.nsplit * p.G * D);
+  // this thread's rows of the scores
+  float* const dst = sp.scores + (size_t)unit * p.S_max + k0 + 4 * tid;
+  const int left = n - 4 * tid;
+  const bool quad = left >= 4 && (p.S_max & 3) == 0;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (quad) acc = *reinterpret_cast<const float4*>(dst);
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int h0 = 0; h0 < p.G; h0 += kAccHeads) {
     const int nh = min(kAccHeads, p.G - h0);
     float4 x[kAccBatch];
     auto ask = [&](int h) {  // rows from n on hold anything: their sums are not used
 #pragma unroll
       for (int i = 0; i < kAccBatch; ++i)
-        if (h + i < nh && 4 * tid < n)
+        if (h + i < nh && left > 0)
           x[i] = __ldcg(reinterpret_cast<const float4*>(x0 + (size_t)(h0 + h + i) * sp.x_stride));
     };
     ask(0);
+    // columns of heads h0 .. h0 + nh - 1, `width` at a time: a power of two, so that as many threads as possible
+    // share the splits
+    const int c0 = max(part * per, h0 * (D / 4)), c1 = min(min(part * per + per, cols), (h0 + nh) * (D / 4));
+    int width = 1;
+    while (width < min(c1 - c0, kAccThreads)) width *= 2;
+    const int slots = kAccThreads / width;
+    const int cc = tid % width, slot = tid / width;
     if (h0 > 0) __syncthreads();
     for (int h = warp; h < nh; h += kAccThreads / 32) {
-      const float2* ptr = p.ws_ml + (size_t)unit * p.nsplit * p.G + h0 + h;
+      const float2* ptr = unit_ml + h0 + h;
       float M = -INFINITY, L = 0.f;
 #pragma unroll 4
       for (int s = lane; s < ns; s += 32) {
@@ -334,32 +350,25 @@ __global__ void __launch_bounds__(kAccThreads, 4)
       for (int i = 0; i < kAccBatch; ++i) {
         if (h + i < nh) {
           const float2 z = ml[h + i];
-          acc.x = fmaf(fast_exp2(x[i].x - z.x), z.y, acc.x);
-          acc.y = fmaf(fast_exp2(x[i].y - z.x), z.y, acc.y);
-          acc.z = fmaf(fast_exp2(x[i].z - z.x), z.y, acc.z);
-          acc.w = fmaf(fast_exp2(x[i].w - z.x), z.y, acc.w);
+          sum.x = fmaf(fast_exp2(x[i].x - z.x), z.y, sum.x);
+          sum.y = fmaf(fast_exp2(x[i].y - z.x), z.y, sum.y);
+          sum.z = fmaf(fast_exp2(x[i].z - z.x), z.y, sum.z);
+          sum.w = fmaf(fast_exp2(x[i].w - z.x), z.y, sum.w);
         }
       }
     }
     if (ns > 1) {
-      // columns of heads h0 .. h0 + nh - 1
-      const int c0 = max(part * per, h0 * (D / 4)), c1 = min(min(part * per + per, cols), (h0 + nh) * (D / 4));
-      int width = 1;  // columns at a time: a power of two, so that as many threads as possible share the splits
-      while (width < min(c1 - c0, kAccThreads)) width *= 2;
-      const int slots = kAccThreads / width;
-      const int cc = tid % width, slot = tid / width;
       for (int c = c0; c < c1; c += width) {
         const int col = c + cc;
         const int h = col / (D / 4);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         if (col < c1) {
           const float top = ml[h - h0].x;
-          const size_t base = (size_t)unit * p.nsplit * p.G + h;
-          const float4* src = reinterpret_cast<const float4*>(p.ws_o + base * D) + (col - h * (D / 4));
+          const float4* src = unit_o + col;  // column col of split 0: head h, dims 4 (col - h D / 4)
 #pragma unroll 4
           for (int s = slot; s < ns; s += slots) {
-            const float f = fast_exp2(__ldcg(&p.ws_ml[base + (size_t)s * p.G].x) - top);
-            const float4 v = __ldcg(src + (size_t)s * p.G * (D / 4));
+            const float f = fast_exp2(__ldcg(&unit_ml[(size_t)s * p.G + h].x) - top);
+            const float4 v = __ldcg(src + (size_t)s * cols);
             o.x = fmaf(v.x, f, o.x);
             o.y = fmaf(v.y, f, o.y);
             o.z = fmaf(v.z, f, o.z);
@@ -389,14 +398,11 @@ __global__ void __launch_bounds__(kAccThreads, 4)
       }
     }
   }
-  float* dst = sp.scores + (size_t)unit * p.S_max + k0 + 4 * tid;
-  const int left = n - 4 * tid;
-  if (left >= 4 && (p.S_max & 3) == 0) {
-    float4 v = *reinterpret_cast<const float4*>(dst);
-    v.x += acc.x, v.y += acc.y, v.z += acc.z, v.w += acc.w;
-    *reinterpret_cast<float4*>(dst) = v;
+  if (quad) {
+    acc.x += sum.x, acc.y += sum.y, acc.z += sum.z, acc.w += sum.w;
+    *reinterpret_cast<float4*>(dst) = acc;
   } else {
-    const float a[4] = {acc.x, acc.y, acc.z, acc.w};
+    const float a[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (j < left) dst[j] += a[j];
