@@ -220,7 +220,7 @@ bool plan_evict(EvictPlan& pl, int B, int K, int S_max, int keep) {
   pl.fused = pl.cta && pl.max_moves <= gqa::kEvFusedMoves;
   const int seg = ((S_max + gqa::kEvCluster - 1) / gqa::kEvCluster + 31) / 32 * 32;
   pl.seg_keys = std::min(seg, gqa::kEvMaxSegKeys);
-  pl.done_off = pl.fused ? 0 : ((size_t)B * K * (1 + 2 * (size_t)pl.max_moves) * sizeof(int32_t) + 15) / 16 * 16;
+  pl.done_off = pl.fused ? 0 : ((size_t)B * K * (1 + 4 * (size_t)pl.max_moves) * sizeof(int32_t) + 15) / 16 * 16;
   pl.bytes = pl.done_off + (pl.fused ? (size_t)std::max(B, 1) * sizeof(unsigned long long) : 0);
   return true;
 }
@@ -266,6 +266,7 @@ int kv_evict_impl(void* k_cache, void* v_cache, float* scores, int32_t* row_pos,
   p.sinks = sinks;
   p.max_moves = pl.max_moves;
   p.seg_keys = pl.seg_keys;
+  p.quads = S_max % 4 == 0 && aligned16(row_pos);
   p.row_chunks = d * (dtype == GQA_F32 ? 4 : 2) / 16;
   if (pc) {
     p.block_table = pc->table;

@@ -19,6 +19,9 @@
 //     shared memory (S_max 131072: 8 CTAs of 64 KB). tau by a radix select, 11
 //     + 11 + 10 bits, the histograms summed over the cluster through
 //     distributed shared memory.
+//     The movers' scores and positions go to the workspace with their numbers,
+//     so that the rows past keep can be cleared at once, by the threads that
+//     own them.
 //   evict_move_kernel    all CTAs of the GPU, a group of lanes per row: sources
 //     lie at or above keep and destinations below it, so no order is needed.
 //
@@ -26,6 +29,8 @@
 #pragma once
 
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "decode.cuh"
@@ -40,7 +45,8 @@ constexpr int kEvFusedMoves = 512;
 constexpr int kEvBins = 2048;
 constexpr int kEvCopies = 4;         // histograms of a CTA: fewer warps meet in a bin
 constexpr int kEvCluster = 8;
-constexpr int kEvStaticBytes = (kEvCopies * kEvBins + 4 * kEvWarps + 16) * 4;
+constexpr int kEvFine = 32;          // bins of a coarse bin: a cluster sums the coarse ones, then one's fine ones
+constexpr int kEvStaticBytes = ((kEvCopies + 2) * kEvBins + 2 * (kEvBins / kEvFine) + 4 * kEvWarps + 16) * 4;
 // keys of a segment kept in shared memory; rows past these (caches of more than 8 x 40960 rows) are read again
 constexpr int kEvMaxSegKeys = 40960;
 
@@ -50,11 +56,13 @@ struct EvictParams {
   int32_t* row_pos;  // or null
   int32_t* seqlens;
   const int32_t* recent_from;  // or null
-  int32_t* ws;                 // per unit: [0] number of moves, then max_moves sources, then max_moves destinations
+  int32_t* ws;                 // per unit: the number of moves, then max_moves each of sources, destinations,
+                               // scores (float bits) and positions
   unsigned long long* done;    // fused moves: [B] tagged counters of the heads that are done
   unsigned long long tag;
   const int32_t* block_table;
   int B, K, S_max, keep, sinks, max_moves, seg_keys;
+  int quads;  // scores and positions may be read four at a time
   int num_blocks, block_size, max_blocks, row_chunks, ctas_per_unit;
 };
 
@@ -114,6 +122,18 @@ __device__ __forceinline__ void evict_move_rows(const EvictParams& p, int b, int
   }
 }
 
+// Mover i of the unit: its row, score and position to the workspace
+__device__ __forceinline__ void evict_save(const EvictParams& p, int32_t* list, int i, int t, float score, int pos) {
+  list[1 + i] = t;
+  list[1 + 2 * (size_t)p.max_moves + i] = __float_as_int(score);
+  if (p.row_pos) list[1 + 3 * (size_t)p.max_moves + i] = pos;
+}
+
+__device__ __forceinline__ void evict_clear(const EvictParams& p, size_t at) {
+  p.scores[at] = 0.f;
+  if (p.row_pos) p.row_pos[at] = -1;
+}
+
 // Sum of v over the lanes below n, and over all
 __device__ __forceinline__ int2 below_and_all(int v, int n) {
   const int lane = threadIdx.x & 31;
@@ -132,7 +152,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_cta_kernel(const EvictParams
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_wait();
   grid_dep_launch();
-  int32_t* list = p.ws + (size_t)unit * (1 + 2 * (size_t)p.max_moves);
+  int32_t* list = p.ws + (size_t)unit * (1 + 4 * (size_t)p.max_moves);
   const int len = p.seqlens[b];
   const long long recent = p.recent_from ? (long long)p.recent_from[b] : 1ll << 32;
   if (len <= p.keep || len > p.S_max) {
@@ -218,8 +238,16 @@ __global__ void __launch_bounds__(kEvThreads) evict_cta_kernel(const EvictParams
   const int moves = m.y;
   holes = h.x;
   movers = m.x;
-  int32_t* from = kFused ? moved : list + 1;
   int32_t* to = kFused ? moved + kEvFusedMoves : list + 1 + p.max_moves;
+  float score[J];
+  int pos[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {  // the separate moves' scores and positions, asked for together
+    const int t = row0 + j * 32;
+    const bool ask = !kFused && t >= p.keep && t < end;
+    score[j] = ask ? p.scores[base + t] : 0.f;
+    pos[j] = ask && p.row_pos ? p.row_pos[base + t] : 0;
+  }
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int t = row0 + j * 32;
@@ -227,39 +255,43 @@ __global__ void __launch_bounds__(kEvThreads) evict_cta_kernel(const EvictParams
     const bool hole = t < min(end, p.keep) && !s, mover = t >= p.keep && s;
     const unsigned below = (1u << lane) - 1u;
     const unsigned hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, mover);
-    if (mover) from[movers + __popc(mb & below)] = t;
+    if (mover) {
+      const int i = movers + __popc(mb & below);
+      if (kFused)
+        moved[i] = t;
+      else
+        evict_save(p, list, i, t, score[j], pos[j]);
+    }
     if (hole) to[holes + __popc(hb & below)] = t;
+    if (!kFused && t >= p.keep && t < end) evict_clear(p, base + t);
     holes += __popc(hb);
     movers += __popc(mb);
   }
-  __syncthreads();  // (the workspace's lists too: written and read by this CTA)
-
-  // ---- scores and positions along with their rows, then the rows past keep
-  for (int i = tid; i < moves; i += kEvThreads) {
-    p.scores[base + to[i]] = p.scores[base + from[i]];
-    if (p.row_pos) p.row_pos[base + to[i]] = p.row_pos[base + from[i]];
+  if (!kFused) {
+    if (tid == 0) list[0] = moves;
+    return;
   }
-  if (kFused) {
+  __syncthreads();
+
+  // ---- rows, scores and positions, then the rows past keep
+  for (int i = tid; i < moves; i += kEvThreads) {
+    p.scores[base + to[i]] = p.scores[base + moved[i]];
+    if (p.row_pos) p.row_pos[base + to[i]] = p.row_pos[base + moved[i]];
+  }
+  {
     const int lanes = 2 * p.row_chunks;  // K's chunks, then V's
     evict_move_rows(p, b, g, tid % lanes, tid / lanes, kEvThreads / lanes, moves, [&](int i) { return moved[i]; },
                     [&](int i) { return moved[kEvFusedMoves + i]; });
   }
   __syncthreads();
-  for (int t = p.keep + tid; t < len; t += kEvThreads) {
-    p.scores[base + t] = 0.f;
-    if (p.row_pos) p.row_pos[base + t] = -1;
-  }
+  for (int t = p.keep + tid; t < len; t += kEvThreads) evict_clear(p, base + t);
   if (tid == 0) {
-    if (!kFused) {
-      list[0] = moves;
-    } else {
-      // the length: written once every head of the sequence has read it
+    // the length: written once every head of the sequence has read it
+    __threadfence();
+    if (take_ticket(p.done + b, p.tag) == p.K) {
       __threadfence();
-      if (take_ticket(p.done + b, p.tag) == p.K) {
-        __threadfence();
-        p.seqlens[b] = p.keep;
-        *reinterpret_cast<volatile unsigned long long*>(p.done + b) = 0ull;  // a replay repeats the tag
-      }
+      p.seqlens[b] = p.keep;
+      *reinterpret_cast<volatile unsigned long long*>(p.done + b) = 0ull;  // a replay repeats the tag
     }
   }
 }
@@ -269,7 +301,9 @@ __global__ void __cluster_dims__(kEvCluster, 1, 1) __launch_bounds__(kEvThreads)
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint32_t ev_smem[];
   uint32_t* hist = ev_smem;                                              // [kEvCopies][kEvBins]
-  int* wcount = reinterpret_cast<int*>(ev_smem + kEvCopies * kEvBins);   // [4][kEvWarps]
+  uint32_t* sums = hist + kEvCopies * kEvBins;                           // [pass parity][kEvBins] the copies' sums
+  uint32_t* coarse = sums + 2 * kEvBins;                                 // [pass parity][kEvBins / kEvFine]
+  int* wcount = reinterpret_cast<int*>(coarse + 2 * (kEvBins / kEvFine));  // [4][kEvWarps]
   int* shared = wcount + 4 * kEvWarps;                                   // [16] CTA totals and results
   uint32_t* keys = reinterpret_cast<uint32_t*>(shared + 16);             // [seg_keys]
   cg::cluster_group cl = cg::this_cluster();
@@ -280,7 +314,7 @@ __global__ void __cluster_dims__(kEvCluster, 1, 1) __launch_bounds__(kEvThreads)
   grid_dep_wait();
   grid_dep_launch();
 
-  int32_t* list = p.ws + (size_t)unit * (1 + 2 * (size_t)p.max_moves);
+  int32_t* list = p.ws + (size_t)unit * (1 + 4 * (size_t)p.max_moves);
   const int len = p.seqlens[b];
   if (len <= p.keep || len > p.S_max) {  // the same in every CTA of the cluster
     if (rank == 0 && tid == 0) {
@@ -297,8 +331,8 @@ __global__ void __cluster_dims__(kEvCluster, 1, 1) __launch_bounds__(kEvThreads)
   auto key_of = [&](int i) {  // key of row t0 + i
     return i < held ? keys[i] : evict_key(p, base, t0 + i, recent);
   };
-#pragma unroll 4
-  for (int i = tid; i < held; i += kEvThreads) keys[i] = evict_key(p, base, t0 + i, recent);
+  uint32_t* mine = hist + (warp % kEvCopies) * kEvBins;
+  for (int i = tid; i < kEvCopies * kEvBins; i += kEvThreads) hist[i] = 0u;
   __syncthreads();
 
   // ---- tau, the keep-th largest key, and how many rows equal to it stay
@@ -306,61 +340,111 @@ __global__ void __cluster_dims__(kEvCluster, 1, 1) __launch_bounds__(kEvThreads)
   int need = p.keep;
   constexpr int kShift[3] = {21, 10, 0};
   constexpr int kBits[3] = {11, 11, 10};
+  // the keys, and the first histogram with them
+  const int quads = p.quads ? held / 4 : 0;
+#pragma unroll 4
+  for (int i = tid; i < quads; i += kEvThreads) {
+    const float4 sc = *reinterpret_cast<const float4*>(p.scores + base + t0 + 4 * i);
+    int4 at = make_int4(t0 + 4 * i, t0 + 4 * i + 1, t0 + 4 * i + 2, t0 + 4 * i + 3);
+    if (p.row_pos) at = *reinterpret_cast<const int4*>(p.row_pos + base + t0 + 4 * i);
+    auto key = [&](float v, int pos) { return pos < p.sinks || pos >= recent ? 0xffffffffu : score_key(v); };
+    const uint4 k = make_uint4(key(sc.x, at.x), key(sc.y, at.y), key(sc.z, at.z), key(sc.w, at.w));
+    reinterpret_cast<uint4*>(keys)[i] = k;
+    atomicAdd(&mine[k.x >> kShift[0]], 1u);
+    atomicAdd(&mine[k.y >> kShift[0]], 1u);
+    atomicAdd(&mine[k.z >> kShift[0]], 1u);
+    atomicAdd(&mine[k.w >> kShift[0]], 1u);
+  }
+  for (int i = 4 * quads + tid; i < t1 - t0; i += kEvThreads) {
+    const uint32_t k = evict_key(p, base, t0 + i, recent);
+    if (i < held) keys[i] = k;
+    atomicAdd(&mine[k >> kShift[0]], 1u);
+  }
+
   bool exact = false;  // as many keys with this prefix or above as rows stay
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     if (exact) break;
     const int nb = 1 << kBits[pass];
-    for (int i = tid; i < kEvCopies * kEvBins; i += kEvThreads) hist[i] = 0u;
-    __syncthreads();
-    uint32_t* mine = hist + (warp % kEvCopies) * kEvBins;
+    uint32_t* sum = sums + (pass & 1) * kEvBins;
+    if (pass > 0) {
+      for (int i = tid; i < kEvCopies * kEvBins; i += kEvThreads) hist[i] = 0u;
+      __syncthreads();
+      auto add = [&](uint32_t k) {
+        if ((k & mask) == prefix) atomicAdd(&mine[(k >> kShift[pass]) & (nb - 1)], 1u);
+      };
 #pragma unroll 4
-    for (int i = tid; i < t1 - t0; i += kEvThreads) {
-      const uint32_t k = key_of(i);
-      if ((k & mask) == prefix) atomicAdd(&mine[(k >> kShift[pass]) & (nb - 1)], 1u);
+      for (int i = tid; i < held / 4; i += kEvThreads) {
+        const uint4 k = reinterpret_cast<const uint4*>(keys)[i];
+        add(k.x), add(k.y), add(k.z), add(k.w);
+      }
+      for (int i = held / 4 * 4 + tid; i < t1 - t0; i += kEvThreads) add(key_of(i));
     }
     __syncthreads();
-    // bins 2 x and 2 x + 1, x counted from the top by thread: first over the copies, then over the cluster
-    const int x = nb / 2 - 1 - tid;
-    if (x >= 0) {
+    // bins 2 tid and 2 tid + 1: the copies' sums, and 16 lanes' coarse bin
+    if (tid < nb / 2) {
       uint2 c = make_uint2(0u, 0u);
 #pragma unroll
       for (int i = 0; i < kEvCopies; ++i) {
-        const uint2 v = reinterpret_cast<const uint2*>(hist + i * kEvBins)[x];
+        const uint2 v = reinterpret_cast<const uint2*>(hist + i * kEvBins)[tid];
         c.x += v.x, c.y += v.y;
       }
-      reinterpret_cast<uint2*>(hist)[x] = c;
+      reinterpret_cast<uint2*>(sum)[tid] = c;
+      uint32_t all = c.x + c.y;
+#pragma unroll
+      for (int off = kEvFine / 4; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+      if ((lane & 15) == 0) coarse[(pass & 1) * (kEvBins / kEvFine) + tid / 16] = all;
     }
+    // (a sum's second use comes after the next pass's: every CTA has read its first by then)
     cl.sync();
-    int c[2] = {0, 0};  // bin 2 x + 1, bin 2 x
-    if (x >= 0) {
+    if (warp == 0) {
+      // the bin, counted from the top, that the need-th key lies in: among the coarse ones (two a lane), then among
+      // its fine ones. c0: the higher of the lane's bins, c1: the lower
+      auto find = [&](int c0, int c1, int want, int& at, int& above, int& count) {
+        int incl = c0 + c1;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += o;
+        }
+        const int before = incl - c0 - c1;
+        const unsigned hit = __ballot_sync(0xffffffffu, before < want && incl >= want);  // one lane
+        const int who = __ffs(hit) - 1;
+        const bool low = before + c0 < want;
+        at = __shfl_sync(0xffffffffu, 2 * lane + (low ? 1 : 0), who);
+        above = __shfl_sync(0xffffffffu, low ? before + c0 : before, who);
+        count = __shfl_sync(0xffffffffu, low ? c1 : c0, who);
+      };
+      const int nc = nb / kEvFine;  // 64 or 32
+      int c0 = 0, c1 = 0;
 #pragma unroll
       for (int r = 0; r < kEvCluster; ++r) {
-        const uint2 v = reinterpret_cast<const uint2*>(cl.map_shared_rank(hist, r))[x];
-        c[0] += (int)v.y, c[1] += (int)v.x;
+        const uint32_t* v = cl.map_shared_rank(coarse, r) + (pass & 1) * (kEvBins / kEvFine);
+        if (2 * lane < nc) {
+          c0 += (int)v[nc - 1 - 2 * lane];
+          c1 += (int)v[nc - 2 - 2 * lane];
+        }
       }
-    }
-    int incl = c[0] + c[1];  // inclusive scan over threads: keys in this thread's bins or higher
+      int group, above, count, fine, fine_above;
+      find(c0, c1, need, group, above, count);
+      group = nc - 1 - group;
+      c0 = 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
-    }
-    if (lane == 31) wcount[warp] = incl;
-    __syncthreads();
-    const int above = below_and_all(wcount[lane], warp).x + incl - c[0] - c[1];  // keys in higher bins than this thread's
-    if (above < need && above + c[0] + c[1] >= need) {  // exactly one thread
-      const bool first = above + c[0] >= need;
-      shared[0] = 2 * x + (first ? 1 : 0);
-      shared[1] = need - above - (first ? 0 : c[0]);
-      shared[5] = shared[1] == c[first ? 0 : 1];
+      for (int r = 0; r < kEvCluster; ++r)
+        c0 += (int)cl.map_shared_rank(sum, r)[group * kEvFine + kEvFine - 1 - lane];
+      find(c0, 0, need - above, fine, fine_above, count);
+      if (lane == 0) {
+        shared[0] = group * kEvFine + kEvFine - 1 - fine / 2;
+        shared[1] = need - above - fine_above;
+        shared[5] = shared[1] == count;
+      }
     }
     __syncthreads();
     prefix |= (uint32_t)shared[0] << kShift[pass];
     mask |= (uint32_t)(nb - 1) << kShift[pass];
     need = shared[1];
     exact = shared[5] != 0 && prefix != 0;
-    cl.sync();  // every CTA has read this histogram
+    __syncthreads();  // before they are written again
   }
   // the rows above tau stay, and of those equal to it the first need_eq
   const uint32_t tau = exact ? prefix - 1 : prefix;
@@ -385,33 +469,67 @@ __global__ void __cluster_dims__(kEvCluster, 1, 1) __launch_bounds__(kEvThreads)
   }
 
   // ---- holes and movers, counted and then numbered
-  auto sweep = [&](int holes, int movers, bool write) {
+  // kBatch x 32 rows at a time: the rows' scores and positions, if they are to be written, are all asked for first
+  constexpr int kBatch = 4;
+  auto sweep = [&](int holes, int movers, auto write) {
     int e = eq_before;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-      const int i = i0 + lane;
-      const bool in = i < w1;
-      const uint32_t k = in ? key_of(i) : 0u;
-      const bool is_eq = in && k == tau;
-      const unsigned below = (1u << lane) - 1u;
-      const unsigned em = __ballot_sync(0xffffffffu, is_eq);
-      const bool stays = in && (k > tau || (is_eq && e + __popc(em & below) < need_eq));
-      e += __popc(em);
-      const int t = t0 + i;
-      const bool hole = in && t < p.keep && !stays, mover = in && t >= p.keep && stays;
-      const unsigned hm = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
-      if (write) {
-        if (mover) list[1 + movers + __popc(mm & below)] = t;
-        if (hole) list[1 + p.max_moves + holes + __popc(hm & below)] = t;
+    for (int i0 = w0; i0 < w1; i0 += 32 * kBatch) {
+      float score[kBatch];
+      int pos[kBatch];
+      if constexpr (write.value) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int i = i0 + 32 * u + lane, t = t0 + i;
+          const bool ask = i < w1 && t >= p.keep && key_of(i) >= tau;
+          score[u] = ask ? p.scores[base + t] : 0.f;
+          pos[u] = ask && p.row_pos ? p.row_pos[base + t] : 0;
+        }
       }
-      holes += __popc(hm);
-      movers += __popc(mm);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + 32 * u + lane;
+        const bool in = i < w1;
+        const uint32_t k = in ? key_of(i) : 0u;
+        const bool is_eq = in && k == tau;
+        const unsigned below = (1u << lane) - 1u;
+        const unsigned em = __ballot_sync(0xffffffffu, is_eq);
+        const bool stays = in && (k > tau || (is_eq && e + __popc(em & below) < need_eq));
+        e += __popc(em);
+        const int t = t0 + i;
+        const bool hole = in && t < p.keep && !stays, mover = in && t >= p.keep && stays;
+        const unsigned hm = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
+        if constexpr (write.value) {
+          if (mover) evict_save(p, list, movers + __popc(mm & below), t, score[u], pos[u]);
+          if (hole) list[1 + p.max_moves + holes + __popc(hm & below)] = t;
+        }
+        holes += __popc(hm);
+        movers += __popc(mm);
+      }
     }
     return make_int2(holes, movers);
   };
-  const int2 mine = sweep(0, 0, false);
+  int2 found;
+  if (need_eq == 0 && held == t1 - t0) {  // no ties, all keys at hand: no order is needed to count
+    int below = 0, beyond = 0;
+    const int first = p.keep - t0;  // row t0 + i is below keep for i < first
+#pragma unroll 2
+    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+      const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+      const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < w1) {
+          below += kk[j] <= tau && i + j < first;
+          beyond += kk[j] > tau && i + j >= first;
+        }
+    }
+    found = make_int2(warp_sum(below), warp_sum(beyond));
+  } else {
+    found = sweep(0, 0, std::false_type());
+  }
   if (lane == 0) {
-    wcount[kEvWarps + warp] = mine.x;
-    wcount[2 * kEvWarps + warp] = mine.y;
+    wcount[kEvWarps + warp] = found.x;
+    wcount[2 * kEvWarps + warp] = found.y;
   }
   __syncthreads();
   const int2 hw = below_and_all(wcount[kEvWarps + lane], warp), mw = below_and_all(wcount[2 * kEvWarps + lane], warp);
@@ -424,22 +542,21 @@ __global__ void __cluster_dims__(kEvCluster, 1, 1) __launch_bounds__(kEvThreads)
   const int oh = lane < kEvCluster ? other[3] : 0, om = lane < kEvCluster ? other[4] : 0;
   const int holes = hw.x + warp_sum(lane < rank ? oh : 0), movers = mw.x + warp_sum(lane < rank ? om : 0);
   const int moves = warp_sum(om);
-  sweep(holes, movers, true);
-  __threadfence();
-  cl.sync();  // the lists are complete, and no CTA reads another's shared memory from here on
-
-  // ---- scores and positions along with their rows, then the rows past keep
-  for (int i = rank * kEvThreads + tid; i < moves; i += kEvCluster * kEvThreads) {
-    const int src = __ldcg(list + 1 + i), dst = __ldcg(list + 1 + p.max_moves + i);
-    p.scores[base + dst] = p.scores[base + src];
-    if (p.row_pos) p.row_pos[base + dst] = p.row_pos[base + src];
-  }
-  cl.sync();
-  for (int t = p.keep + rank * kEvThreads + tid; t < len; t += kEvCluster * kEvThreads) {
-    p.scores[base + t] = 0.f;
-    if (p.row_pos) p.row_pos[base + t] = -1;
-  }
+  cl.barrier_arrive();  // done with the other CTAs' shared memory
+  sweep(holes, movers, std::true_type());
   if (rank == 0 && tid == 0) list[0] = moves;
+  __syncthreads();  // the movers' scores have been read
+  const int clear0 = max(t0, p.keep);
+  const int quad0 = p.quads ? (clear0 + 3) / 4 : 0, quad1 = p.quads ? t1 / 4 : 0;  // of four rows each
+  for (int i = quad0 + tid; i < quad1; i += kEvThreads) {
+    reinterpret_cast<float4*>(p.scores + base)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.row_pos) reinterpret_cast<int4*>(p.row_pos + base)[i] = make_int4(-1, -1, -1, -1);
+  }
+  const bool any = quad0 < quad1;
+  for (int t = clear0 + tid; t < (any ? min(t1, 4 * quad0) : t1); t += kEvThreads) evict_clear(p, base + t);
+  if (any)
+    for (int t = 4 * quad1 + tid; t < t1; t += kEvThreads) evict_clear(p, base + t);
+  cl.barrier_wait();
 }
 
 constexpr int kEvMoveThreads = 256;
@@ -457,8 +574,14 @@ __global__ void __launch_bounds__(kEvMoveThreads) evict_move_kernel(const EvictP
     const int len = p.seqlens[b];
     if (len > p.keep && len <= p.S_max) p.seqlens[b] = p.keep;
   }
-  const int32_t* list = p.ws + (size_t)unit * (1 + 2 * (size_t)p.max_moves);
+  const int32_t* list = p.ws + (size_t)unit * (1 + 4 * (size_t)p.max_moves);
   const int moves = __ldcg(list);
+  const size_t base = (size_t)unit * p.S_max, mm = p.max_moves;
+  for (int i = part * kEvMoveThreads + threadIdx.x; i < moves; i += p.ctas_per_unit * kEvMoveThreads) {
+    const int to = __ldcg(list + 1 + mm + i);
+    p.scores[base + to] = __int_as_float(__ldcg(list + 1 + 2 * mm + i));
+    if (p.row_pos) p.row_pos[base + to] = __ldcg(list + 1 + 3 * mm + i);
+  }
   const int lanes = 2 * p.row_chunks, per_cta = kEvMoveThreads / lanes;  // K's chunks, then V's
   evict_move_rows(p, b, g, threadIdx.x % lanes, part * per_cta + threadIdx.x / lanes, p.ctas_per_unit * per_cta, moves,
                   [&](int i) { return __ldcg(list + 1 + i); }, [&](int i) { return __ldcg(list + 1 + p.max_moves + i); });
