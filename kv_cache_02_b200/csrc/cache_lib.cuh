@@ -212,11 +212,15 @@ struct EvictPlan {
   size_t done_off = 0, bytes = 0;
 };
 
-bool plan_evict(EvictPlan& pl, int B, int K, int S_max, int keep) {
+bool plan_evict(EvictPlan& pl, int B, int K, int S_max, int keep, int sms) {
   if (B < 0 || K <= 0 || S_max <= 0 || keep <= 0 || keep > S_max) return false;
   if ((long long)B * K * gqa::kEvCluster >= (1ll << 31)) return false;
   pl.max_moves = std::min(keep, S_max - keep);
-  pl.cta = S_max <= gqa::kEvCtaRows;
+  // a CTA per (b, g) while 8 rows a thread hold the cache (8 heads of 8192 rows: 18 us, as clusters 25); up to 16
+  // where the clusters are more than the GPU holds at once (64 heads of 16384 rows: 32 us against 58; 8 of them: 35
+  // against 21)
+  pl.cta = S_max <= gqa::kEvCtaRows / 2 ||
+           (S_max <= gqa::kEvCtaRows && (long long)B * K * gqa::kEvCluster > sms);
   pl.fused = pl.cta && pl.max_moves <= gqa::kEvFusedMoves;
   const int seg = ((S_max + gqa::kEvCluster - 1) / gqa::kEvCluster + 31) / 32 * 32;
   pl.seg_keys = std::min(seg, gqa::kEvMaxSegKeys);
@@ -233,7 +237,8 @@ int launch_evict_cta(const gqa::EvictParams& p, cudaStream_t st) {
   if (p.S_max <= gqa::kEvThreads) return run(gqa::evict_cta_kernel<1, kFused>);
   if (p.S_max <= 2 * gqa::kEvThreads) return run(gqa::evict_cta_kernel<2, kFused>);
   if (p.S_max <= 4 * gqa::kEvThreads) return run(gqa::evict_cta_kernel<4, kFused>);
-  return run(gqa::evict_cta_kernel<8, kFused>);
+  if (p.S_max <= 8 * gqa::kEvThreads) return run(gqa::evict_cta_kernel<8, kFused>);
+  return run(gqa::evict_cta_kernel<16, kFused>);
 }
 
 int kv_evict_impl(void* k_cache, void* v_cache, float* scores, int32_t* row_pos, int32_t* seqlens,
@@ -243,7 +248,7 @@ int kv_evict_impl(void* k_cache, void* v_cache, float* scores, int32_t* row_pos,
   if (B < 0 || K <= 0 || S_max <= 0 || sinks < 0) return GQA_ERR_INVALID_ARG;
   if (keep <= 0 || keep > S_max || (d != 64 && d != 128)) return GQA_ERR_SHAPE;
   EvictPlan pl;
-  if (!plan_evict(pl, B, K, S_max, keep)) return GQA_ERR_SHAPE;
+  if (!plan_evict(pl, B, K, S_max, keep, sm_count(current_device()))) return GQA_ERR_SHAPE;
   if (B == 0) return GQA_OK;
   if (!k_cache || !v_cache || !scores || !seqlens) return GQA_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(scores)) return GQA_ERR_ALIGN;
@@ -530,7 +535,7 @@ int gqa_decode_scores_paged(void* out, float* scores, const void* q, const void*
 
 size_t gqa_kv_evict_workspace_bytes(int B, int K, int S_max, int keep) {
   EvictPlan pl;
-  return plan_evict(pl, B, K, S_max, keep) ? pl.bytes : 0;
+  return plan_evict(pl, B, K, S_max, keep, sm_count(current_device())) ? pl.bytes : 0;
 }
 
 int gqa_kv_evict(void* k_cache, void* v_cache, float* scores, int32_t* row_pos, int32_t* seqlens,

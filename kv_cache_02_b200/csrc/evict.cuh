@@ -7,7 +7,7 @@
 // it. Then the holes (rows below keep that go) and the movers (rows from keep
 // on that stay) are numbered in order of their rows: mover i goes to hole i.
 //
-//   evict_cta_kernel     bounded caches (kEvCtaRows rows): a CTA per (b, g),
+//   evict_cta_kernel     bounded caches (at most kEvCtaRows): a CTA per (b, g),
 //     keys in registers. tau two bits a round, the counts of three candidates
 //     exchanged behind one barrier; as soon as one of them counts keep rows,
 //     that is the answer (random scores: about 11 of 16 rounds). With few
@@ -40,7 +40,7 @@ namespace gqa {
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 static_assert(kEvWarps == 32, "a lane per warp joins the warps' counts");
-constexpr int kEvCtaRows = 8192;     // evict_cta_kernel: up to 8 rows a thread
+constexpr int kEvCtaRows = 16384;    // evict_cta_kernel: up to 16 rows a thread
 constexpr int kEvFusedMoves = 512;
 constexpr int kEvBins = 2048;
 constexpr int kEvCopies = 4;         // histograms of a CTA: fewer warps meet in a bin

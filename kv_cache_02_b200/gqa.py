@@ -387,11 +387,10 @@ def _call(name, tensors, scalars, stream, strided=None, after=None) -> None:
     if len(devices) != 1:
         raise ValueError("tensors must be on one device")
     dev, = devices
-    if strided is None:
-        dense = all(map(_is_contiguous, given))
-    else:
-        dense = all(t is None or t.is_contiguous() for t in tensors[:strided.start] + tensors[strided.stop:])
-    if not dense:
+    dense = given
+    if strided is not None:
+        dense = [t for t in tensors[:strided.start] + tensors[strided.stop:] if t is not None]
+    if not all(map(_is_contiguous, dense)):
         raise ValueError("tensors must be contiguous")
     ptrs = [None if t is None else t.data_ptr() for t in tensors]
     if after is not None:

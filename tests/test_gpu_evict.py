@@ -66,6 +66,8 @@ CASES = [
     (1, 2, 8193, 128, synth.BF16, (8193,), 700, 4, 64, True),           # a cluster of CTAs
     (2, 1, 9000, 128, synth.BF16, (40, 9000), 39, 0, 0, False),         # a long cache, a short sequence
     (1, 2, 20000, 64, synth.BF16, (19999,), 15000, 1, 1000, False),
+    (3, 8, 10004, 64, synth.BF16, (10004, 9000, 12), 9000, 4, 64, True),  # more heads than clusters fit: 16 rows a thread
+    (3, 8, 16384, 64, synth.BF16, (16384, 16000, 9), 16200, 4, 64, False),
 ]
 
 
