@@ -47,7 +47,8 @@ GQA_API int gqa_rope_table(float* rope, int max_pos, int rotary_dim, double thet
  *   with j = i + rotary_dim / 2, or for interleaved != 0 the pair (2 i, 2 i + 1);
  *   dims from rotary_dim on are not rotated.
  *
- * float32 arithmetic, one rounding to dtype at the end.
+ * float32 arithmetic (a row's squares and their sum have to lie in its range),
+ * one rounding to dtype at the end.
  *
  * q, k, v    : T new tokens of each of B sequences; token n = b * T + t
  *              starts q_stride (k_stride, v_stride) elements after token
@@ -141,7 +142,8 @@ GQA_API int gqa_decode_scores_paged(void* out, float* scores, const void* q, con
  *           leaves the sequence's scores as they are.
  * scores  : [B, K, S_max] float32, in place; rows t >= len_b are neither
  *           read nor written. Results repeat bit for bit.
- * GQA_BF16 only. workspace: gqa_prompt_scores_workspace_bytes(...) bytes.
+ * GQA_BF16 only, H / K at most 128 (GQA_ERR_SHAPE). workspace:
+ * gqa_prompt_scores_workspace_bytes(...) bytes.
  */
 GQA_API size_t gqa_prompt_scores_workspace_bytes(int B, int T, int H, int K, int S_max, int d);
 GQA_API int gqa_prompt_scores(float* scores, const void* q, const void* k_cache, const int32_t* seqlens, int B, int T,

@@ -10,6 +10,10 @@
 // the splits: their outputs, and the scores as weights. Reading K again
 // instead would cost 2 d bytes a key; the scores are 8 G bytes a key written
 // and read back, mostly in L2.
+//
+// Measured: 8 x 8192 keys of 32 and 8 heads, d 128: 50 us (gqa_decode: 43; the
+// bytes of K and V at a copy's rate: 41); one sequence of 131072 keys, 64 and 8
+// heads: 106 us (82; 82), of which the join takes 20: 33 MB of scores.
 #pragma once
 
 #include "decode.cuh"

@@ -25,7 +25,11 @@
 //   evict_move_kernel    all CTAs of the GPU, a group of lanes per row: sources
 //     lie at or above keep and destinations below it, so no order is needed.
 //
-// Bytes: 8 per row read (score, position), and the moved rows twice.
+// Bytes: 8 per row read (score, position), and the moved rows twice. Measured:
+// 64 heads cut from about 2080 rows to 2048, one launch: 10 us; 8 heads from
+// 131072 rows to 8192: select 27 us, move 17 us (62 MB in rows of 256 bytes).
+// What is left of the select is one cluster barrier and two reads of other
+// CTAs' histograms a pass (3 us), and 16 keys a thread looked at five times.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -577,10 +577,12 @@ __global__ void prompt_lse_kernel(float* __restrict__ nlse, const float2* __rest
   for (long long r = blockIdx.x * (long long)blockDim.x + threadIdx.x; r < rows;
        r += (long long)gridDim.x * blockDim.x) {
     float M = -INFINITY, L = 0.f;
-    for (int s = 0; s < splits; ++s) M = fmaxf(M, __ldcg(&ml[s * rows + r].x));
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
       const float2 v = __ldcg(&ml[s * rows + r]);
-      if (v.y != 0.f) L += v.y * fast_exp2(v.x - M);
+      const float mn = fmaxf(M, v.x);
+      if (mn != -INFINITY) L = L * fast_exp2(M - mn) + v.y * fast_exp2(v.x - mn);  // (-inf, 0): nothing was seen
+      M = mn;
     }
     nlse[r] = L == 0.f ? -INFINITY : -(M + log2f(L));
   }
