@@ -207,16 +207,16 @@ GQA_API int gqa_kv_evict_paged(void* k_pool, void* v_pool, const int32_t* block_
  *
  * gqa_kv_append_mxfp4 quantizes T new tokens' rows k_new, v_new ([B, T, K, d]
  * bfloat16) into rows pos[b] .. pos[b] + T - 1: 2^(E - 127) is the largest
- * power of two not above the block's largest magnitude, over 4 (E = 0 for a
- * block of zeros); code = x / 2^(E - 127) rounded to nearest, ties to the
+ * power of two not above the block's largest magnitude, over 4 (E = 0 where
+ * that lies below 2^-127); code = x / 2^(E - 127) rounded to nearest, ties to the
  * even code, magnitudes beyond 6 to 6, the sign kept. A block that holds a
  * NaN or an infinity gets E = 255 and codes 0: its values are NaN. pos[b] < 0
  * or pos[b] + T > S_max sets GQA_DEVERR_APPEND_POS and leaves that sequence's
  * rows unwritten.
  *
  * gqa_kv_read_mxfp4 reads rows pos[b] .. pos[b] + T - 1 back as bfloat16
- * ([B, T, K, d]; every value is exact), for a prefill that goes on from a
- * cached prompt. Out of range: GQA_DEVERR_APPEND_POS, zeros.
+ * ([B, T, K, d]; exact, but for codes of a foreign writer whose value passes
+ * bfloat16's largest: infinity), for a prefill that goes on from a cached prompt. Out of range: GQA_DEVERR_APPEND_POS, zeros.
  *
  * gqa_decode_mxfp4 is gqa_decode over the values the 4-bit cache holds: q and
  * out are [B, H, d] bfloat16, everything else as for gqa_decode. Rows

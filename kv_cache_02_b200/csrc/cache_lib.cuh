@@ -385,22 +385,23 @@ int launch_prompt(const PromptPlan& pl, gqa::PromptParams p, const void* q, cons
       !encode_rows_bf16(&tk, k_cache, (uint64_t)p.B * p.K * p.S_max, D, gqa::kPsRows))
     return GQA_ERR_CUDA;
   using C = gqa::PsCfg<D>;
+  const auto rows_kernel = gqa::prompt_scores_kernel<D, gqa::kPsKindRows, false>;
+  const auto keys_kernel = gqa::prompt_scores_kernel<D, gqa::kPsKindKeys, false>;
+  const auto keys_zero_kernel = gqa::prompt_scores_kernel<D, gqa::kPsKindKeys, true>;
   static DeviceCache configured{};
   const int dev = current_device();
   if (dev >= 0 && dev < kMaxDevices && configured[dev].load(std::memory_order_acquire) == 0) {
-    if (cudaFuncSetAttribute(gqa::prompt_scores_kernel<D, gqa::kPsKindRows>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(gqa::prompt_scores_kernel<D, gqa::kPsKindKeys>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
-      return GQA_ERR_CUDA;
+    for (auto kernel : {rows_kernel, keys_kernel, keys_zero_kernel})
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+        return GQA_ERR_CUDA;
     configured[dev].store(1, std::memory_order_release);
   }
   const int units = p.B * p.K;
   const int sms = sm_count(dev);
   p.splits = pl.key_splits;
   p.items = units * ((p.n_rt + 1) / 2) * p.splits;
-  int rc = gqa::launch_kernel(gqa::prompt_scores_kernel<D, gqa::kPsKindRows>, (unsigned)std::min(p.items, sms),
-                              gqa::kPsThreads, C::kSmemBytes, st, true, tq, tk, p);
+  int rc = gqa::launch_kernel(rows_kernel, (unsigned)std::min(p.items, sms), gqa::kPsThreads, C::kSmemBytes, st, true,
+                              tq, tk, p);
   if (rc != GQA_OK) return rc;
   if (p.splits > 1) {
     const long long rows = (long long)units * p.n_rt * gqa::kPsRows;
@@ -411,8 +412,8 @@ int launch_prompt(const PromptPlan& pl, gqa::PromptParams p, const void* q, cons
   p.splits = pl.row_splits;
   p.items = units * ((p.n_kt + 1) / 2) * p.splits;
   p.queue += 2;
-  rc = gqa::launch_kernel(gqa::prompt_scores_kernel<D, gqa::kPsKindKeys>, (unsigned)std::min(p.items, sms),
-                          gqa::kPsThreads, C::kSmemBytes, st, true, tq, tk, p);
+  rc = gqa::launch_kernel(p.tile_tokens * p.G == gqa::kPsRows ? keys_kernel : keys_zero_kernel,
+                          (unsigned)std::min(p.items, sms), gqa::kPsThreads, C::kSmemBytes, st, true, tq, tk, p);
   if (rc != GQA_OK || p.splits == 1) return rc;
   return gqa::launch_kernel(gqa::prompt_add_kernel, (unsigned)grid_for((long long)units * p.S_max, 256, sms), 256, 0,
                             st, true, p.scores, (const float*)p.part, p.seqlens, units, p.K, p.S_max, p.splits);

@@ -15,7 +15,7 @@
 // be q.
 //
 // Measured: 4 x 4096 tokens of 32 + 8 heads, d 128, bfloat16, no cache: 73 us,
-// 4.70 TB/s, 0.72 of a copy; issue slots 70 % used at 16 resident warps a
+// 4.70 TB/s, 0.72 of a copy; issue slots 70 % used at 7 warps a
 // scheduler. R = 2 takes 125 us, 8 77 us, 5 81 us; persistent blocks that load
 // the next token's rows ahead need 96 to 116 registers and take 80 to 115 us.
 // A decode step of 8 tokens into a paged cache: 2.6 us in a graph.

@@ -195,7 +195,8 @@ __device__ __forceinline__ float exp2_sum32(const float (&y)[32]) {
   return s0 + s1;
 }
 
-template <int D, int kKind>
+// kZeroRows: G does not divide 128 (a look at every tile's sums: 4 % at 7 heads a group, 4 to 8 % at 3)
+template <int D, int kKind, bool kZeroRows>
 __global__ void __launch_bounds__(kPsThreads, 1)
     prompt_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const PromptParams p) {
@@ -470,7 +471,8 @@ __global__ void __launch_bounds__(kPsThreads, 1)
           bool again = true;
           if (!first) {
             s = pass(m == -INFINITY ? 0.f : m);
-            again = __any_sync(0xffffffffu, !(s < 1e30f));  // the reference lies far below
+            // the reference lies far below, or there was none: keys at -inf alone so far
+            again = __any_sync(0xffffffffu, !(s < 1e30f) || (m == -INFINITY && s != 0.f));
           }
           if (again) {
             float top = -INFINITY;
@@ -498,32 +500,40 @@ __global__ void __launch_bounds__(kPsThreads, 1)
           const int tok0 = (it.begin + j) * p.tile_tokens;
           auto cmin_of = [&](int off) { return min(max(off - tok0, -1), kPsRows) * p.G - h * 64; };
           const int cmin = cmin_of(key_off + lane);
-          const bool odd = tok0 < p.T - it.len || tok0 + p.tile_tokens > p.T;
-          const bool all = !odd && cmin_of(key_off + 31) <= 0;
+          bool odd = tok0 < p.T - it.len || tok0 + p.tile_tokens > p.T;
+          float s;
+          for (;;) {
+            s = 0.f;
+            const bool all = !odd && cmin_of(key_off + 31) <= 0;
 #pragma unroll 1
-          for (int c = max(cmin_of(key_off), 0) >> 5; c < 2; ++c) {  // from the first column that any key sees
-            float x[32];
-            tmem_ld32(col + c * 32, x);
-            tc_wait_ld();
+            for (int c = max(cmin_of(key_off), 0) >> 5; c < 2; ++c) {  // from the first column that any key sees
+              float x[32];
+              tmem_ld32(col + c * 32, x);
+              tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const ulonglong2 zz = *reinterpret_cast<const ulonglong2*>(ls + c * 32 + i);
-              f2_get(f2_fma(f2(x[i], x[i + 1]), scale2, zz.x), x[i], x[i + 1]);
-              f2_get(f2_fma(f2(x[i + 2], x[i + 3]), scale2, zz.y), x[i + 2], x[i + 3]);
-            }
-            if (!all) {
-              const int from = cmin - c * 32;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < from) x[i] = -INFINITY;
-              if (odd) {  // rows that do not count hold anything, NaN included
+              for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 zz = *reinterpret_cast<const ulonglong2*>(ls + c * 32 + i);
+                f2_get(f2_fma(f2(x[i], x[i + 1]), scale2, zz.x), x[i], x[i + 1]);
+                f2_get(f2_fma(f2(x[i + 2], x[i + 3]), scale2, zz.y), x[i + 2], x[i + 3]);
+              }
+              if (!all) {
+                const int from = cmin - c * 32;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (ls[c * 32 + i] == -INFINITY) x[i] = -INFINITY;
+                  if (i < from) x[i] = -INFINITY;
+                if (odd) {  // rows that do not count hold anything, NaN included
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (ls[c * 32 + i] == -INFINITY) x[i] = -INFINITY;
+                }
               }
+              s += exp2_sum32<false>(x);
             }
-            l += exp2_sum32<false>(x);
+            // a tile's zero rows are NaN with an infinite key: the tile once more, without them
+            if (!kZeroRows || odd || !__any_sync(0xffffffffu, s != s && key < it.len)) break;
+            odd = true;
           }
+          l += s;
         }
         tc_fence_before();
         __syncwarp();

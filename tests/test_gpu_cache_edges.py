@@ -198,3 +198,53 @@ def test_empty_calls(gqa):
     gqa.gqa_kv_append_mxfp4(*c, z(0, 3, 2, D), z(0, 3, 2, D), z(0, dtype=i32))
     gqa.gqa_decode_mxfp4(z(0, 8, D), z(0, 8, D), *c, z(0, dtype=i32), 1.0)
     assert gqa.gqa_get_last_error() == (0, 0)
+
+
+@pytest.mark.parametrize("H,d", [(4, 128), (3, 128), (5, 64), (7, 128)])  # 7 heads: 126 rows of a tile are queries
+def test_prompt_scores_of_keys_at_minus_infinity(gqa, H, d):
+    # such a key weighs nothing, whether it is alone among others or all that a query sees of the first tiles
+    B, T, K, S, n = 1, 60, 1, 800, 777
+    k = synth.normal((B, K, S, d), synth.F32, 0x3620, 2)
+    q = synth.normal((B, T, H, d), synth.F32, 0x3620, 1)
+    q[..., 0] = 1.0
+    k[..., 0] = 0.0
+    finite = host(dev(k).bfloat16())
+    k[0, 0, [*range(200), 333, 650], 0] = -np.inf
+    kb, qb = dev(k).bfloat16(), dev(q).bfloat16()
+    scores = torch.zeros(B, K, S, device="cuda")
+    ws = torch.empty(gqa.gqa_prompt_scores_workspace_bytes(B, T, H, K, S, d), dtype=torch.uint8, device="cuda")
+    gqa.gqa_prompt_scores(scores, qb, kb, torch.tensor([n], dtype=torch.int32, device="cuda"), d ** -0.5, workspace=ws)
+    assert gqa.gqa_get_last_error() == (0, 0)
+    added = cache_ops.prompt_scores(host(qb), host(kb), (n,), d ** -0.5)
+    assert not added[0, 0, :200].any() and added[0, 0, 200:333].all() and np.isfinite(added).all()
+    # a weight: 2 d 2^-23 scale max sum |q k| + 2^-20 (the scores' tests); T H of them added up
+    qa, ka = np.abs(oracle.widen(host(qb))), np.abs(oracle.widen(finite))
+    big = d ** -0.5 * np.sqrt((qa * qa).sum(-1).max() * (ka * ka).sum(-1).max())
+    rel = 2 * d * 2.0 ** -23 * big + 2.0 ** -20 + T * H * 2.0 ** -24
+    assert np.all(np.abs(host(scores)[0, 0] - added[0, 0]) <= rel * added[0, 0])
+
+
+def test_decode_scores_paged_entries_outside_the_pool(gqa):
+    # block 0 is read in place of a bad entry; the other sequence, and entries past the length, do not mind
+    B, H, K, d, bs, mb = 2, 8, 2, 128, 16, 8
+    pools = [dev(synth.normal((B * mb, K, bs, d), synth.BF16, 0x3621, s)) for s in (2, 3)]
+    q = dev(synth.normal((B, H, d), synth.BF16, 0x3621, 1))
+    table = torch.arange(B * mb, dtype=torch.int32, device="cuda").reshape(B, mb).contiguous()
+    lens = torch.tensor([128, 70], dtype=torch.int32, device="cuda")
+    ws = torch.empty(gqa.gqa_decode_scores_paged_workspace_bytes(B, H, K, d, bs, mb), dtype=torch.uint8, device="cuda")
+
+    def run():
+        out, scores = torch.empty_like(q), torch.zeros(B, K, mb * bs, device="cuda")
+        gqa.gqa_decode_scores_paged(out, scores, q, *pools, table, lens, 0.1, workspace=ws)
+        return out, scores, gqa.gqa_get_last_error()
+
+    out, scores, err = run()
+    assert err == (0, 0)
+    table[1, 5:] = -1  # past the length
+    table[0, 3] = B * mb
+    out2, scores2, err = run()
+    assert err == (gqa.GQA_ERR_DEVICE, gqa.GQA_DEVERR_BLOCK)
+    assert torch.equal(out2[1], out[1]) and torch.equal(scores2[1], scores[1])
+    table[0, 3] = 0
+    out3, scores3, err = run()
+    assert err == (0, 0) and torch.equal(out2, out3) and torch.equal(scores2, scores3)
