@@ -72,11 +72,13 @@ __device__ __forceinline__ void warp_tile_scores(WarpState<D>& st, const uint32_
     mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
   }
   const float mn_a = fmaxf(st.m_a, mx_a), mn_b = fmaxf(st.m_b, mx_b);
-  const float al_a = fast_exp2(st.m_a - mn_a), al_b = fast_exp2(st.m_b - mn_b);
+  // keys at -inf alone so far: they weigh nothing, against any finite reference
+  const float r_a = mn_a == -INFINITY ? 0.f : mn_a, r_b = mn_b == -INFINITY ? 0.f : mn_b;
+  const float al_a = fast_exp2(st.m_a - r_a), al_b = fast_exp2(st.m_b - r_b);
   st.m_a = mn_a;
   st.m_b = mn_b;
-  const float p0 = fast_exp2(x0 - mn_a), p1 = fast_exp2(x1 - mn_b);
-  const float p2 = fast_exp2(x2 - mn_a), p3 = fast_exp2(x3 - mn_b);
+  const float p0 = fast_exp2(x0 - r_a), p1 = fast_exp2(x1 - r_b);
+  const float p2 = fast_exp2(x2 - r_a), p3 = fast_exp2(x3 - r_b);
   st.l_a = st.l_a * al_a + p0 + p2;
   st.l_b = st.l_b * al_b + p1 + p3;
 #pragma unroll
@@ -120,6 +122,11 @@ __device__ __forceinline__ void scores_epilogue(const DecodeParams& p, const Ite
     const int h = i / D, dim = i % D;
     float M, L, O;
     merged<D>(merge, h, dim, M, L, O);
+    if (M == -INFINITY) {  // every key of the item is at -inf, or NaN: 0, or NaN
+      L = 0.f;
+      for (int w = 0; w < kDecConsumerWarps; ++w) L += merge[(kDecConsumerWarps + w) * kDecHeadsPerCta + h];
+      O = L;
+    }
     if (single)
       out_row[i] = __float2bfloat16_rn(O / L);
     else
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(kAccThreads, 4)
       for (int s = lane; s < ns; s += 32) {
         const float2 v = __ldcg(&ptr[(size_t)s * p.G]);
         const float mn = fmaxf(M, v.x);
-        L = L * fast_exp2(M - mn) + v.y * fast_exp2(v.x - mn);
+        L = mn == -INFINITY ? L + v.y : L * fast_exp2(M - mn) + v.y * fast_exp2(v.x - mn);  // (-inf, 0 or NaN)
         M = mn;
       }
       float top = M;

@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(kPsThreads, 1)
         const float2 o = *mine;
         if (kKind == kPsKindRows) {
           const float M = fmaxf(m, o.x);
-          float L = 0.f;
-          if (M != -INFINITY) L = l * fast_exp2(m - M) + o.y * fast_exp2(o.x - M);
+          // M = -inf: nothing seen, or keys at -inf (0), or NaN
+          const float L = M == -INFINITY ? l + o.y : l * fast_exp2(m - M) + o.y * fast_exp2(o.x - M);
           const size_t row = ((size_t)it.unit * p.n_rt + 2 * it.pair + t) * kPsRows + r;
           if (t >= it.subs) {
             // no such tile
@@ -591,7 +591,7 @@ __global__ void prompt_lse_kernel(float* __restrict__ nlse, const float2* __rest
     for (int s = 0; s < splits; ++s) {
       const float2 v = __ldcg(&ml[s * rows + r]);
       const float mn = fmaxf(M, v.x);
-      if (mn != -INFINITY) L = L * fast_exp2(M - mn) + v.y * fast_exp2(v.x - mn);  // (-inf, 0): nothing was seen
+      L = mn == -INFINITY ? L + v.y : L * fast_exp2(M - mn) + v.y * fast_exp2(v.x - mn);  // (-inf, 0 or NaN)
       M = mn;
     }
     nlse[r] = L == 0.f ? -INFINITY : -(M + log2f(L));

@@ -217,11 +217,49 @@ def test_prompt_scores_of_keys_at_minus_infinity(gqa, H, d):
     assert gqa.gqa_get_last_error() == (0, 0)
     added = cache_ops.prompt_scores(host(qb), host(kb), (n,), d ** -0.5)
     assert not added[0, 0, :200].any() and added[0, 0, 200:333].all() and np.isfinite(added).all()
-    # a weight: 2 d 2^-23 scale max sum |q k| + 2^-20 (the scores' tests); T H of them added up
-    qa, ka = np.abs(oracle.widen(host(qb))), np.abs(oracle.widen(finite))
-    big = d ** -0.5 * np.sqrt((qa * qa).sum(-1).max() * (ka * ka).sum(-1).max())
-    rel = 2 * d * 2.0 ** -23 * big + 2.0 ** -20 + T * H * 2.0 ** -24
-    assert np.all(np.abs(host(scores)[0, 0] - added[0, 0]) <= rel * added[0, 0])
+    rel = 2 * d * 2.0 ** -23 * largest(host(qb), finite, d ** -0.5) + 2.0 ** -20
+    assert_scores(host(scores), np.zeros((B, K, S), np.float32), added, (n,), rel, T * H + S, "keys at -inf")
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2])
+@pytest.mark.parametrize("H,d", [(8, 128), (3, 64)])
+def test_decode_scores_of_keys_at_minus_infinity(gqa, H, d, splits):
+    B, K, S, n = 1, 1, 800, 777
+    k, v, q = (synth.normal(shape, synth.F32, 0x3622, s) for s, shape in ((2, (B, K, S, d)), (3, (B, K, S, d)),
+                                                                          (1, (B, H, d))))
+    q[..., 0] = 1.0
+    k[..., 0] = 0.0
+    finite = host(dev(k).bfloat16())
+    k[0, 0, [*range(450), 500, 776], 0] = -np.inf
+    kb, vb, qb = (dev(x).bfloat16() for x in (k, v, q))
+    scores, out = torch.zeros(B, K, S, device="cuda"), torch.empty_like(qb)
+    ws = torch.empty(gqa.gqa_decode_scores_workspace_bytes(B, H, K, S, d, splits), dtype=torch.uint8, device="cuda")
+    gqa.gqa_decode_scores(out, scores, qb, kb, vb, torch.tensor([n], dtype=torch.int32, device="cuda"), d ** -0.5,
+                          splits, workspace=ws)
+    assert gqa.gqa_get_last_error() == (0, 0)
+    want, added, spread = cache_ops.decode_scores(host(qb), host(kb), host(vb), (n,), d ** -0.5)
+    assert not added[0, 0, :450].any() and added[0, 0, 450:500].all() and np.isfinite(want).all()
+    rel = 2 * d * 2.0 ** -23 * largest(host(qb), finite, d ** -0.5) + 2.0 ** -20
+    assert_scores(host(scores), np.zeros((B, K, S), np.float32), added, (n,), rel, H + S, "keys at -inf")
+    assert_out(host(out), want, spread, rel, "keys at -inf")
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+def test_a_split_of_nan_keys_is_not_lost(gqa, splits):
+    # every query sees them: outputs and weights are NaN, whatever the other splits hold
+    B, H, K, d, S, n, bad = 1, 6, 2, 128, 4000, 3999, 2100
+    k = synth.normal((B, K, S, d), synth.F32, 0x3623, 2)
+    k[0, 0, :bad] = np.nan
+    kb, q = dev(k).bfloat16(), dev(synth.normal((B, 4, H, d), synth.BF16, 0x3623, 1))
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    a, b, out = torch.zeros(B, K, S, device="cuda"), torch.zeros(B, K, S, device="cuda"), torch.empty_like(q[:, 0])
+    ws = torch.empty(max(gqa.gqa_decode_scores_workspace_bytes(B, H, K, S, d, splits),
+                         gqa.gqa_prompt_scores_workspace_bytes(B, 4, H, K, S, d)), dtype=torch.uint8, device="cuda")
+    gqa.gqa_decode_scores(out, a, q[:, 0].contiguous(), kb, kb.nan_to_num(), lens, 0.1, splits, workspace=ws)
+    gqa.gqa_prompt_scores(b, q, kb, lens, 0.1, workspace=ws)
+    assert out[0, :H // K].isnan().all() and out[0, H // K:].isfinite().all()
+    for s, seen in ((a, n), (b, n - 3)):
+        assert s[0, 0, :seen].isnan().all() and s[0, 1].isfinite().all() and not s[0, :, n:].any()
 
 
 def test_decode_scores_paged_entries_outside_the_pool(gqa):
