@@ -162,7 +162,10 @@ int decode_scores_impl(void* out, float* scores, const void* q, const void* k_ca
   if (!plan_scores(sp, B, H, K, S_max, d, num_splits, pc != nullptr, sm_count(current_device()))) return GQA_ERR_SHAPE;
   if (!workspace || workspace_bytes < sp.bytes) return GQA_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return GQA_ERR_ALIGN;
-  const long long chunks = (S_max + gqa::kAccKeys - 1) / gqa::kAccKeys;
+  // the join: four rows a thread, or eight where those CTAs would not all be resident (four per SM)
+  const int acc_keys = 4 * gqa::kAccThreads;
+  const bool eight = (long long)B * K * ((S_max + acc_keys - 1) / acc_keys) > 4ll * sm_count(current_device());
+  const long long chunks = eight ? (S_max + 2 * acc_keys - 1) / (2 * acc_keys) : (S_max + acc_keys - 1) / acc_keys;
   if ((long long)B * K * chunks >= (1ll << 31)) return GQA_ERR_SHAPE;
   const DecodePlan& pl = sp.pl;
   char* ws = static_cast<char*>(workspace);
@@ -199,8 +202,11 @@ int decode_scores_impl(void* out, float* scores, const void* q, const void* k_ca
   int rc = d == 128 ? launch_scores_decode<128>(sp, p, x, k_cache, v_cache, rows, st)
                     : launch_scores_decode<64>(sp, p, x, k_cache, v_cache, rows, st);
   if (rc != GQA_OK) return rc;
-  return gqa::launch_kernel(d == 128 ? gqa::scores_finish_kernel<128> : gqa::scores_finish_kernel<64>,
-                            (unsigned)(B * K * chunks), gqa::kAccThreads, 0, st, true, p, x, (int)chunks);
+  auto finish = [&](auto kernel) {
+    return gqa::launch_kernel(kernel, (unsigned)(B * K * chunks), gqa::kAccThreads, 0, st, true, p, x, (int)chunks);
+  };
+  if (d == 128) return eight ? finish(gqa::scores_finish_kernel<128, 2>) : finish(gqa::scores_finish_kernel<128, 1>);
+  return eight ? finish(gqa::scores_finish_kernel<64, 2>) : finish(gqa::scores_finish_kernel<64, 1>);
 }
 
 // ----------------------------------------------------------------------------

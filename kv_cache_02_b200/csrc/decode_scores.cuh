@@ -11,9 +11,9 @@
 // instead would cost 2 d bytes a key; the scores are 8 G bytes a key written
 // and read back, mostly in L2.
 //
-// Measured: 8 x 8192 keys of 32 and 8 heads, d 128: 50 us (gqa_decode: 43; the
+// Measured: 8 x 8192 keys of 32 and 8 heads, d 128: 49 us (gqa_decode: 43; the
 // bytes of K and V at a copy's rate: 41); one sequence of 131072 keys, 64 and 8
-// heads: 106 us (82; 82), of which the join takes 20: 33 MB of scores.
+// heads: 98 us (82; 82), the join of 33 MB of scores included.
 #pragma once
 
 #include "decode.cuh"
@@ -278,23 +278,24 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   }
 }
 
-// The join. A CTA takes kAccKeys rows of one unit. Its warps first join the
+// The join. A CTA takes 4 Q rows a thread of one unit. Its warps first join the
 // splits' (m, l) of the group's heads; then a thread adds up the heads'
-// weights of four rows, in order of the heads, and the unit's output columns
+// weights of its rows, in order of the heads, and the unit's output columns
 // are shared out among the unit's CTAs, a CTA's threads over the splits of its
 // columns (summed in a fixed order). Latency bounds it: all that does not
-// depend on (m, l) is asked for first.
+// depend on (m, l) is asked for first, the scores to be added to into L2 (their
+// values in registers would make them spill). Q = 2 where the CTAs of Q = 1
+// would not all be resident (131072 keys of 8 heads: 98 us a call, for 107).
 constexpr int kAccThreads = 256;
-constexpr int kAccKeys = 1024;
 constexpr int kAccHeads = 64;  // heads whose (M, 1 / L) are held at a time
-constexpr int kAccBatch = 4;   // heads whose scores a thread asks for at once
+constexpr int kAccFlight = 4;  // float4 of scores that a thread asks for at once
 
-template <int D>
+template <int D, int Q>
 __global__ void __launch_bounds__(kAccThreads, 4)
     scores_finish_kernel(const DecodeParams p, const ScoresParams sp, int chunks) {
   __shared__ float2 ml[kAccHeads];
   __shared__ float4 red[kAccThreads];
-  static_assert(kAccKeys == 4 * kAccThreads, "four rows a thread");
+  constexpr int kAccKeys = 4 * Q * kAccThreads, kAccBatch = kAccFlight / Q;
   const int unit = blockIdx.x / chunks, part = blockIdx.x % chunks;
   const int b = unit / p.K, g = unit % p.K;
   const int k0 = part * kAccKeys;
@@ -313,19 +314,25 @@ __global__ void __launch_bounds__(kAccThreads, 4)
   const float4* unit_o = reinterpret_cast<const float4*>(p.ws_o + (size_t)unit * p.nsplit * p.G * D);
   // this thread's rows of the scores
   float* const dst = sp.scores + (size_t)unit * p.S_max + k0 + 4 * tid;
-  const int left = n - 4 * tid;
-  const bool quad = left >= 4 && (p.S_max & 3) == 0;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (quad) acc = *reinterpret_cast<const float4*>(dst);
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kNext = 4 * kAccThreads;  // rows between a thread's quads
+  bool quad[Q];
+  float4 sum[Q];
+#pragma unroll
+  for (int u = 0; u < Q; ++u) {
+    quad[u] = n - 4 * tid - u * kNext >= 4 && (p.S_max & 3) == 0;
+    sum[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (quad[u]) asm volatile("prefetch.global.L2 [%0];" ::"l"(__cvta_generic_to_global(dst + u * kNext)));
+  }
   for (int h0 = 0; h0 < p.G; h0 += kAccHeads) {
     const int nh = min(kAccHeads, p.G - h0);
-    float4 x[kAccBatch];
+    float4 x[Q][kAccBatch];
     auto ask = [&](int h) {  // rows from n on hold anything: their sums are not used
 #pragma unroll
-      for (int i = 0; i < kAccBatch; ++i)
-        if (h + i < nh && left > 0)
-          x[i] = __ldcg(reinterpret_cast<const float4*>(x0 + (size_t)(h0 + h + i) * sp.x_stride));
+      for (int u = 0; u < Q; ++u)
+#pragma unroll
+        for (int i = 0; i < kAccBatch; ++i)
+          if (h + i < nh && n - 4 * tid - u * kNext > 0)
+            x[u][i] = __ldcg(reinterpret_cast<const float4*>(x0 + (size_t)(h0 + h + i) * sp.x_stride + u * kNext));
     };
     ask(0);
     // columns of heads h0 .. h0 + nh - 1, `width` at a time: a power of two, so that as many threads as possible
@@ -361,10 +368,13 @@ __global__ void __launch_bounds__(kAccThreads, 4)
       for (int i = 0; i < kAccBatch; ++i) {
         if (h + i < nh) {
           const float2 z = ml[h + i];
-          sum.x = fmaf(fast_exp2(x[i].x - z.x), z.y, sum.x);
-          sum.y = fmaf(fast_exp2(x[i].y - z.x), z.y, sum.y);
-          sum.z = fmaf(fast_exp2(x[i].z - z.x), z.y, sum.z);
-          sum.w = fmaf(fast_exp2(x[i].w - z.x), z.y, sum.w);
+#pragma unroll
+          for (int u = 0; u < Q; ++u) {
+            sum[u].x = fmaf(fast_exp2(x[u][i].x - z.x), z.y, sum[u].x);
+            sum[u].y = fmaf(fast_exp2(x[u][i].y - z.x), z.y, sum[u].y);
+            sum[u].z = fmaf(fast_exp2(x[u][i].z - z.x), z.y, sum[u].z);
+            sum[u].w = fmaf(fast_exp2(x[u][i].w - z.x), z.y, sum[u].w);
+          }
         }
       }
     }
@@ -376,7 +386,7 @@ __global__ void __launch_bounds__(kAccThreads, 4)
         if (col < c1) {
           const float top = ml[h - h0].x;
           const float4* src = unit_o + col;  // column col of split 0: head h, dims 4 (col - h D / 4)
-#pragma unroll 4
+#pragma unroll(4 / Q)
           for (int s = slot; s < ns; s += slots) {
             const float f = fast_exp2(__ldcg(&unit_ml[(size_t)s * p.G + h].x) - top);
             const float4 v = __ldcg(src + (size_t)s * cols);
@@ -409,14 +419,18 @@ __global__ void __launch_bounds__(kAccThreads, 4)
       }
     }
   }
-  if (quad) {
-    acc.x += sum.x, acc.y += sum.y, acc.z += sum.z, acc.w += sum.w;
-    *reinterpret_cast<float4*>(dst) = acc;
-  } else {
-    const float a[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < left) dst[j] += a[j];
+  for (int u = 0; u < Q; ++u) {
+    if (quad[u]) {
+      float4 acc = *reinterpret_cast<const float4*>(dst + u * kNext);
+      acc.x += sum[u].x, acc.y += sum[u].y, acc.z += sum[u].z, acc.w += sum[u].w;
+      *reinterpret_cast<float4*>(dst + u * kNext) = acc;
+    } else {
+      const float a[4] = {sum[u].x, sum[u].y, sum[u].z, sum[u].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n - 4 * tid - u * kNext) dst[u * kNext + j] += a[j];
+    }
   }
 }
 
