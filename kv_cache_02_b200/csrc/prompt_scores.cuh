@@ -471,8 +471,9 @@ __global__ void __launch_bounds__(kPsThreads, 1)
           bool again = true;
           if (!first) {
             s = pass(m == -INFINITY ? 0.f : m);
-            // the reference lies far below, or there was none: keys at -inf alone so far
-            again = __any_sync(0xffffffffu, !(s < 1e30f) || (m == -INFINITY && s != 0.f));
+            // the reference lies far below, or there is none (keys at -inf alone so far) and the row sees some of these
+            // keys: whatever their sum against 0 is, all of them may lie below 2^-126
+            again = __any_sync(0xffffffffu, !(s < 1e30f) || (m == -INFINITY && lim >= 0));
           }
           if (again) {
             float top = -INFINITY;
