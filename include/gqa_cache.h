@@ -106,6 +106,9 @@ GQA_API int gqa_qk_norm_rope_paged(void* q_out, void* k_out, void* k_pool, void*
  *          what the caller (or gqa_kv_evict) left there, normally 0. The sum
  *          over a group's heads is taken in a fixed order: results repeat
  *          bit for bit.
+ * A key whose score is -inf weighs nothing. A query head that has no other
+ * key adds nothing to the scores and its output is zeros, as for an empty
+ * sequence. A NaN score makes all of its head's weights and its output NaN.
  * The paged form's scores are [B, K, max_blocks * block_size], by logical
  * row. Everything else as for gqa_decode and gqa_decode_paged; GQA_BF16 only
  * (GQA_F32 returns GQA_ERR_UNSUPPORTED).
@@ -142,6 +145,8 @@ GQA_API int gqa_decode_scores_paged(void* out, float* scores, const void* q, con
  *           leaves the sequence's scores as they are.
  * scores  : [B, K, S_max] float32, in place; rows t >= len_b are neither
  *           read nor written. Results repeat bit for bit.
+ * Keys at -inf and NaN as in gqa_decode_scores: a query that sees keys at -inf
+ * alone (the padding of a left-padded prompt, masked by its keys) adds nothing.
  * GQA_BF16 only, H / K at most 128 (GQA_ERR_SHAPE). workspace:
  * gqa_prompt_scores_workspace_bytes(...) bytes.
  */

@@ -128,7 +128,7 @@ __device__ __forceinline__ void scores_epilogue(const DecodeParams& p, const Ite
       O = L;
     }
     if (single)
-      out_row[i] = __float2bfloat16_rn(O / L);
+      out_row[i] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);  // keys at -inf alone: zeros, as without keys
     else
       p.ws_o[(part + h) * D + dim] = O;
     if (dim == 0) p.ws_ml[part + h] = make_float2(M, L);
@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(kAccThreads, 4)
       L = M == -INFINITY ? L : L * fast_exp2(M - top);  // a lane without splits holds 0
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-      if (lane == 0) ml[h] = make_float2(top, 1.f / L);
+      // L = 0: keys at -inf alone, which weigh nothing against any finite maximum
+      if (lane == 0) ml[h] = L == 0.f ? make_float2(0.f, 0.f) : make_float2(top, 1.f / L);
     }
     __syncthreads();
     for (int h = 0; h < nh; h += kAccBatch) {

@@ -74,7 +74,7 @@ struct PsCfg {
 
 struct PromptParams {
   float* scores;   // [B, K, S_max]
-  float* nlse;     // [B * K, n_rt, 128]: -lse; -inf for a row that does not count
+  float* nlse;     // [B * K, n_rt, 128]: -lse; -inf for a row that does not count, or sees keys at -inf alone
   float2* ml;      // key splits > 1: (m, l) [splits, B * K, n_rt, 128]
   float* part;     // row splits > 1: [splits, B * K, S_max]
   unsigned long long* queue;  // [2] this kernel's tagged work counter
@@ -554,13 +554,14 @@ __global__ void __launch_bounds__(kPsThreads, 1)
         const float2 o = *mine;
         if (kKind == kPsKindRows) {
           const float M = fmaxf(m, o.x);
-          // M = -inf: nothing seen, or keys at -inf (0), or NaN
+          // M = -inf: nothing seen, or keys at -inf (0), or NaN. A query without a weight adds nothing: L = 0 is not
+          // divided by, here and in prompt_lse_kernel
           const float L = M == -INFINITY ? l + o.y : l * fast_exp2(m - M) + o.y * fast_exp2(o.x - M);
           const size_t row = ((size_t)it.unit * p.n_rt + 2 * it.pair + t) * kPsRows + r;
           if (t >= it.subs) {
             // no such tile
           } else if (p.splits == 1)
-            p.nlse[row] = pos < 0 ? -INFINITY : -(M + log2f(L));
+            p.nlse[row] = pos < 0 || L == 0.f ? -INFINITY : -(M + log2f(L));
           else
             p.ml[(size_t)it.split * p.B * p.K * p.n_rt * kPsRows + row] =
                 pos < 0 ? make_float2(-INFINITY, 0.f) : make_float2(M, L);
