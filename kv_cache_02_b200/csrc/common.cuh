@@ -231,6 +231,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // have finished and their memory operations are visible. A no-op otherwise.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A kernel launched as a dependent lives while the one before it may still be
+// writing what it will read (lengths that an eviction cuts, rows that a norm or
+// an append has made), so it reads nothing by way of the non-coherent path
+// (__ldg), which is for data that does not change while the kernel lives: plain
+// loads, or L2's (__ldcg) for what is read once.
+
 // Allow the next kernel on the stream, if launched as a programmatic
 // dependent, to be scheduled once every CTA of this grid has got here (or
 // exited).

@@ -164,7 +164,7 @@ __device__ __forceinline__ int paged_row(const DecodeParams& p, int blk, int g, 
 template <bool kPaged>
 __device__ __forceinline__ int kv_row(const DecodeParams& p, int b, int g, int t) {
   if constexpr (!kPaged) return (b * p.K + g) * p.S_max + t;
-  return paged_row(p, __ldg(p.block_table + (size_t)b * p.max_blocks + t / p.block_size), g, t);
+  return paged_row(p, __ldcg(p.block_table + (size_t)b * p.max_blocks + t / p.block_size), g, t);
 }
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
@@ -281,8 +281,8 @@ __device__ __forceinline__ void load_q_frag(uint32_t (&qf)[D / 16][2], const __n
   const uint32_t* qrow = reinterpret_cast<const uint32_t*>(q + (size_t)(hv ? hn : 0) * D);
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
-    const uint32_t lo = __ldg(qrow + ks * 8 + (lane & 3));
-    const uint32_t hi = __ldg(qrow + ks * 8 + 4 + (lane & 3));
+    const uint32_t lo = __ldcg(qrow + ks * 8 + (lane & 3));
+    const uint32_t hi = __ldcg(qrow + ks * 8 + 4 + (lane & 3));
     qf[ks][0] = hv ? lo : 0u;
     qf[ks][1] = hv ? hi : 0u;
   }
@@ -623,7 +623,7 @@ __device__ __forceinline__ DecItem decode_item(const DecodeParams& p, int heads_
   it.unit = rest / p.nsplit;
   it.b = it.unit / p.K;
   it.g = it.unit % p.K;
-  int len = __ldg(p.seqlens + it.b) + p.len_add;
+  int len = __ldcg(p.seqlens + it.b) + p.len_add;
   if (len < 0 || len > p.S_max) {
     if (it.split == 0 && it.hsl == 0 && it.g == 0 && threadIdx.x == 0) raise_error(GQA_DEVERR_SEQLEN);
     len = 0;
@@ -717,13 +717,13 @@ __device__ __forceinline__ void append_row(const DecodeParams& p, const ItemCoor
                                            int lane) {
   using C = DecCfg<D>;
   constexpr int kChunks = D / 8;  // 16-byte chunks per row
-  const int pos = __ldg(p.seqlens + c.b);
+  const int pos = __ldcg(p.seqlens + c.b);
   if (lane < 2 * kChunks) {
     const bool is_v = lane >= kChunks;
     const int ch = is_v ? lane - kChunks : lane;
     const size_t row = (size_t)c.b * p.K + c.g;  // unit (b, g)
-    const uint4 val = __ldg(reinterpret_cast<const uint4*>(
-                                static_cast<const __nv_bfloat16*>(is_v ? p.v_new : p.k_new) + row * D) + ch);
+    const uint4 val = __ldcg(reinterpret_cast<const uint4*>(
+                                 static_cast<const __nv_bfloat16*>(is_v ? p.v_new : p.k_new) + row * D) + ch);
     uint8_t* dst = stage + (is_v ? C::kTileBytes : 0) + (ch >> 3) * C::kHalfBytes + sw128((uint32_t)r, ch & 7);
     *reinterpret_cast<uint4*>(dst) = val;
     if (c.hsl == 0) {  // one head slice writes the cache
@@ -771,7 +771,7 @@ __device__ __forceinline__ void produce_paged(const DecodeParams& p, uint8_t* sm
     const int item = k == 0 ? (int)blockIdx.x : (int)gridDim.x + ticket - 1;
     if (ticket <= 0 || item >= p.nitems) break;
     const ItemCoord c = item_coord(p, item);
-    const int raw = __ldg(p.seqlens + c.b);
+    const int raw = __ldcg(p.seqlens + c.b);
     const int len = valid_len(raw + p.len_add, p.S_max);
     if (lane == 0 && c.g == 0 && c.split == 0 && c.hsl == 0) {
       if (p.len_add ? (raw < 0 || raw >= p.S_max) : (len != raw))
@@ -790,7 +790,7 @@ __device__ __forceinline__ void produce_paged(const DecodeParams& p, uint8_t* sm
     const int32_t* trow = p.block_table + (size_t)c.b * p.max_blocks;
     const int blk_end = (t_end - 1) / bs + 1;  // the item's blocks: [t_begin / bs, blk_end)
     int win = t_begin / bs;                    // lane j holds the entry of block win + j
-    int ent = win + lane < blk_end ? __ldg(trow + win + lane) : 0;
+    int ent = win + lane < blk_end ? __ldcg(trow + win + lane) : 0;
     for (int tt = 0; tt < ntiles && ok; ++tt, ++it) {
       const int s = it % C::kStages;
       const int t0 = t_begin + tt * kDecTileKeys;
@@ -798,7 +798,7 @@ __device__ __forceinline__ void produce_paged(const DecodeParams& p, uint8_t* sm
       const int last_blk = (t0 + rows - 1) / bs;
       if (last_blk >= win + 32) {  // the tile's blocks are past the window: the next 32
         win = t0 / bs;
-        ent = win + lane < blk_end ? __ldg(trow + win + lane) : 0;
+        ent = win + lane < blk_end ? __ldcg(trow + win + lane) : 0;
       }
       if (lane == 0 && it >= C::kStages) ok = mbar_wait_bounded(&empty[s], ((it / C::kStages) - 1) & 1);
       ok = __shfl_sync(kAll, ok ? 1 : 0, 0) != 0;
@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         const int item = k == 0 ? (int)blockIdx.x : (int)gridDim.x + ticket - 1;
         if (ticket <= 0 || item >= p.nitems) break;
         const ItemCoord c = item_coord(p, item);
-        const int raw = __ldg(p.seqlens + c.b);
+        const int raw = __ldcg(p.seqlens + c.b);
         const int len = valid_len(raw + p.len_add, p.S_max);
         if (c.g == 0 && c.split == 0 && c.hsl == 0) {
           if (p.len_add ? (raw < 0 || raw >= p.S_max) : (len != raw)) {
@@ -1235,7 +1235,7 @@ __global__ void __launch_bounds__(NT) decode_combine_kernel(OutT* __restrict__ o
   const int bh = blockIdx.x / CS, slice = blockIdx.x % CS;
   const int b = bh / H, h = bh % H;
   const int g = h / G, j = h % G;
-  const int len = valid_len(__ldg(seqlens + b) + len_add, S_max);
+  const int len = valid_len(__ldcg(seqlens + b) + len_add, S_max);
   const int ns = (len + chunk - 1) / chunk;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int col = tid % RL, slot = tid / RL;

@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kMxDecThreads, kMxCtasPerSm)
       const int item = k == 0 ? (int)blockIdx.x : (int)gridDim.x + ticket - 1;
       if (ticket <= 0 || item >= p.nitems) break;
       const ItemCoord c = item_coord(p, item);
-      const int raw = __ldg(p.seqlens + c.b);
+      const int raw = __ldcg(p.seqlens + c.b);
       const int len = valid_len(raw, p.S_max);
       if (c.g == 0 && c.split == 0 && c.hsl == 0 && len != raw) raise_error(GQA_DEVERR_SEQLEN);
       const int t_begin = c.split * p.chunk;

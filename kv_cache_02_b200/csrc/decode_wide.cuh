@@ -129,7 +129,7 @@ __device__ __forceinline__ void wide_produce_paged(const DecodeParams& p, uint8_
     const int item = k == 0 ? (int)blockIdx.x : (int)gridDim.x + ticket - 1;
     if (ticket <= 0 || item >= p.nitems) break;
     const ItemCoord c = item_coord_n(p, item, kWideHeads);
-    const int raw = __ldg(p.seqlens + c.b);
+    const int raw = __ldcg(p.seqlens + c.b);
     const int len = valid_len(raw + p.len_add, p.S_max);
     if (lane == 0 && c.g == 0 && c.split == 0 && c.hsl == 0 && !p.len_add && len != raw)
       raise_error(GQA_DEVERR_SEQLEN);
@@ -159,7 +159,7 @@ __device__ __forceinline__ void wide_produce_paged(const DecodeParams& p, uint8_
     const int32_t* trow = p.block_table + (size_t)c.b * p.max_blocks;
     const int blk_end = (t_end - 1) / bs + 1;  // the item's blocks: [t_begin / bs, blk_end)
     int win = t_begin / bs;                    // lane j holds the entry of block win + j
-    int ent = win + lane < blk_end ? __ldg(trow + win + lane) : 0;
+    int ent = win + lane < blk_end ? __ldcg(trow + win + lane) : 0;
     for (int tt = 0; tt < ntiles && ok; ++tt, ++it) {
       const int s = it % C::kStages;
       const int t0 = t_begin + tt * kWideKeys;
@@ -167,7 +167,7 @@ __device__ __forceinline__ void wide_produce_paged(const DecodeParams& p, uint8_
       const int last_blk = (t0 + rows - 1) / bs;
       if (last_blk >= win + 32) {  // the tile's blocks are past the window: the next 32
         win = t0 / bs;
-        ent = win + lane < blk_end ? __ldg(trow + win + lane) : 0;
+        ent = win + lane < blk_end ? __ldcg(trow + win + lane) : 0;
       }
       if (lane == 0 && it >= C::kStages) ok = mbar_wait_bounded(&kv_empty[s], ((it / C::kStages) - 1) & 1);
       ok = __shfl_sync(kAll, ok ? 1 : 0, 0) != 0;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int item = k == 0 ? (int)blockIdx.x : (int)gridDim.x + ticket - 1;
         if (ticket <= 0 || item >= p.nitems) break;
         const ItemCoord c = item_coord_n(p, item, kWideHeads);
-        const int raw = __ldg(p.seqlens + c.b);
+        const int raw = __ldcg(p.seqlens + c.b);
         const int len = valid_len(raw + p.len_add, p.S_max);
         if (c.g == 0 && c.split == 0 && c.hsl == 0 && !p.len_add && len != raw) raise_error(GQA_DEVERR_SEQLEN);
         const int t_begin = c.split * p.chunk;

@@ -89,7 +89,7 @@ __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffff
 // Chunk index of row t of unit (b, g), or -1 (a table entry outside the pool).
 __device__ __forceinline__ long long evict_row(const EvictParams& p, int b, int g, int t) {
   if (p.block_table == nullptr) return (((long long)b * p.K + g) * p.S_max + t) * p.row_chunks;
-  const int blk = __ldg(p.block_table + (size_t)b * p.max_blocks + t / p.block_size);
+  const int blk = __ldcg(p.block_table + (size_t)b * p.max_blocks + t / p.block_size);
   if ((unsigned)blk >= (unsigned)p.num_blocks) {
     raise_error(GQA_DEVERR_BLOCK);
     return -1;

@@ -56,7 +56,7 @@ struct ProjParams {
 // (reported by its first token for head 0) and is not written.
 __device__ __forceinline__ bool proj_row(const ProjParams& p, int m, int g, size_t& row) {
   const int b = m / p.T, i = m % p.T;
-  const int p0 = p.pos ? __ldg(p.pos + b) : 0;
+  const int p0 = p.pos ? __ldcg(p.pos + b) : 0;
   if (p0 < 0 || p0 > p.S_max - p.T) {
     if (i == 0 && g == 0) raise_error(GQA_DEVERR_APPEND_POS);
     return false;

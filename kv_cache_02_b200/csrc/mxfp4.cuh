@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kMxThreads)
   for (int y = blockIdx.y; y < 2 * B; y += gridDim.y) {
     const bool is_v = y & 1;
     const int b = y >> 1;
-    const int p0 = __ldg(pos + b);
+    const int p0 = __ldcg(pos + b);
     const uint4* src = reinterpret_cast<const uint4*>((is_v ? v_new : k_new) + (size_t)b * nrows * (2 * kMxD)) + l;
     uint4 w[kMxUnroll][2];
 #pragma unroll
@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(kMxThreads)
       const unsigned r = r0 + i * (kMxThreads / kMxLanes);
       w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
       if (r < nrows) {
-        w[i][0] = __ldg(src + (size_t)r * 16);
-        w[i][1] = __ldg(src + (size_t)r * 16 + 8);
+        w[i][0] = __ldcg(src + (size_t)r * 16);
+        w[i][1] = __ldcg(src + (size_t)r * 16 + 8);
       }
     }
     const bool fits = p0 >= 0 && p0 <= S_max - T;
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kMxThreads)
   for (int y = blockIdx.y; y < 2 * B; y += gridDim.y) {
     const bool is_v = y & 1;
     const int b = y >> 1;
-    const int p0 = __ldg(pos + b);
+    const int p0 = __ldcg(pos + b);
     const bool fits = p0 >= 0 && p0 <= S_max - T;
     if (!fits && !is_v && blockIdx.x == 0 && threadIdx.x == 0) raise_error(GQA_DEVERR_APPEND_POS);
     uint4* out = reinterpret_cast<uint4*>((is_v ? v_out : k_out) + (size_t)b * nrows * (2 * kMxD)) + l;
@@ -175,9 +175,9 @@ __global__ void __launch_bounds__(kMxThreads)
         const unsigned t = r / (unsigned)K, g = r - t * (unsigned)K;
         const size_t at = ((size_t)b * K + g) * S_max + p0 + t;
         const uint32_t* row = reinterpret_cast<const uint32_t*>((is_v ? v_codes : k_codes) + at * kMxRowBytes);
-        codes[i][0] = __ldg(row + l);
-        codes[i][1] = __ldg(row + l + 8);
-        sc[i] = __ldg(reinterpret_cast<const uint32_t*>(is_v ? v_scales : k_scales) + at);
+        codes[i][0] = __ldcg(row + l);
+        codes[i][1] = __ldcg(row + l + 8);
+        sc[i] = __ldcg(reinterpret_cast<const uint32_t*>(is_v ? v_scales : k_scales) + at);
       }
     }
 #pragma unroll

@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
     }
     if (turns) {
       const float* row = p.rope + (size_t)pos * rd + 4 * l;
-      const float4 c4 = __ldg(reinterpret_cast<const float4*>(row));
-      const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + rd / 2));
+      const float4 c4 = *reinterpret_cast<const float4*>(row);
+      const float4 s4 = *reinterpret_cast<const float4*>(row + rd / 2);
       cs[0] = c4.x, cs[1] = c4.y, cs[2] = c4.z, cs[3] = c4.w;
       sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
     }
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
           crow_step = (long long)p.S_max * D;
         } else {
           const int at = row / p.block_size;
-          const int blk = __ldg(p.block_table + (size_t)b * p.max_blocks + at);
+          const int blk = __ldcg(p.block_table + (size_t)b * p.max_blocks + at);
           if ((unsigned)blk < (unsigned)p.num_blocks) {
             crow = ((long long)blk * p.K * p.block_size + (row - at * p.block_size)) * D;
             crow_step = (long long)p.block_size * D;
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
     if (r == 0 || row == p.H) {
       wt = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
       if (wt != nullptr) {
-        Q::unpack(__ldg(reinterpret_cast<const Raw*>(wt + lo)), wv);
-        Q::unpack(__ldg(reinterpret_cast<const Raw*>(wt + hi)), wv + 4);
+        Q::unpack(*reinterpret_cast<const Raw*>(wt + lo), wv);
+        Q::unpack(*reinterpret_cast<const Raw*>(wt + hi), wv + 4);
       }
     }
     if (wt != nullptr) {

@@ -99,7 +99,7 @@ __device__ __forceinline__ PsItem ps_item(const PromptParams& p, int i) {
   const int k = i / p.splits / units;
   it.pair = kKind == kPsKindRows ? pairs - 1 - k : k;  // the longest items first
   it.subs = min(2, tiles - 2 * it.pair);
-  const int len = __ldg(p.seqlens + it.unit / p.K);
+  const int len = __ldcg(p.seqlens + it.unit / p.K);
   it.len = (len < 0 || len > p.S_max) ? 0 : len;
   int first, last;
   if (kKind == kPsKindRows) {
@@ -608,7 +608,7 @@ __global__ void prompt_add_kernel(float* __restrict__ scores, const float* __res
   const long long total = (long long)units * S_max;
   for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
        i += (long long)gridDim.x * blockDim.x) {
-    const int len = __ldg(seqlens + i / S_max / K);
+    const int len = __ldcg(seqlens + i / S_max / K);
     if (len > S_max || i % S_max >= len) continue;
     float s = 0.f;
     for (int k = 0; k < splits; ++k) s += __ldcg(part + k * total + i);
