@@ -9,7 +9,8 @@
  * gqa_get_last_error(). All calls may be captured into a CUDA graph.
  *
  * Workspaces need no initialisation and carry nothing from one call to the
- * next. Two calls (or replays of graphs) that share a workspace must not
+ * next. A size that a gqa_*_workspace_bytes call here returns for a batch of B
+ * also serves every smaller batch of the same other arguments. Two calls (or replays of graphs) that share a workspace must not
  * overlap on the GPU.
  */
 #ifndef GQA_CACHE_H_

@@ -13,6 +13,19 @@ PagedCache paged_cache(const int32_t* table, int num_blocks, int block_size, int
   return pc;
 }
 
+// The workspace sizes that callers ask for: the most that any batch of up to B sequences takes (size(b, SMs), 0 where
+// there is no plan), so that a buffer made for the largest batch serves every smaller one. A smaller batch may take
+// more: its work is split further. From 16 sequences per SM on no plan splits anything (the most that one aims at are
+// 12 work items per SM), and sizes only grow.
+template <typename Size>
+size_t most_over_batches(int B, Size size) {
+  const int sms = sm_count(current_device());
+  size_t most = size(B, sms);
+  if (most == 0) return 0;
+  for (int b = std::min(B, 16 * sms) - 1; b > 0; --b) most = std::max(most, size(b, sms));
+  return most;
+}
+
 // ----------------------------------------------------------------------------
 // gqa_qk_norm_rope
 
@@ -510,17 +523,20 @@ int gqa_qk_norm_rope_paged(void* q_out, void* k_out, void* k_pool, void* v_pool,
 }
 
 size_t gqa_decode_scores_workspace_bytes(int B, int H, int K, int S_max, int d, int num_splits) {
-  ScoresPlan sp;
-  return plan_scores(sp, B, H, K, S_max, d, num_splits, false, sm_count(current_device())) ? sp.bytes : 0;
+  return most_over_batches(B, [&](int b, int sms) {
+    ScoresPlan sp;
+    return plan_scores(sp, b, H, K, S_max, d, num_splits, false, sms) ? sp.bytes : 0;
+  });
 }
 
 size_t gqa_decode_scores_paged_workspace_bytes(int B, int H, int K, int d, int block_size, int max_blocks,
                                                int num_splits) {
   if (block_size <= 0 || block_size % 16 != 0 || max_blocks <= 0 || (long long)max_blocks * block_size >= (1ll << 31))
     return 0;
-  ScoresPlan sp;
-  return plan_scores(sp, B, H, K, max_blocks * block_size, d, num_splits, true, sm_count(current_device())) ? sp.bytes
-                                                                                                         : 0;
+  return most_over_batches(B, [&](int b, int sms) {
+    ScoresPlan sp;
+    return plan_scores(sp, b, H, K, max_blocks * block_size, d, num_splits, true, sms) ? sp.bytes : 0;
+  });
 }
 
 int gqa_decode_scores(void* out, float* scores, const void* q, const void* k_cache, const void* v_cache,
@@ -541,8 +557,10 @@ int gqa_decode_scores_paged(void* out, float* scores, const void* q, const void*
 }
 
 size_t gqa_kv_evict_workspace_bytes(int B, int K, int S_max, int keep) {
-  EvictPlan pl;
-  return plan_evict(pl, B, K, S_max, keep, sm_count(current_device())) ? pl.bytes : 0;
+  return most_over_batches(B, [&](int b, int sms) {
+    EvictPlan pl;
+    return plan_evict(pl, b, K, S_max, keep, sms) ? pl.bytes : 0;
+  });
 }
 
 int gqa_kv_evict(void* k_cache, void* v_cache, float* scores, int32_t* row_pos, int32_t* seqlens,
@@ -596,8 +614,10 @@ int gqa_kv_read_mxfp4(void* k_out, void* v_out, const uint8_t* k_codes, const ui
 }
 
 size_t gqa_prompt_scores_workspace_bytes(int B, int T, int H, int K, int S_max, int d) {
-  PromptPlan pl;
-  return plan_prompt(pl, B, T, H, K, S_max, d, sm_count(current_device())) ? pl.bytes : 0;
+  return most_over_batches(B, [&](int b, int sms) {
+    PromptPlan pl;
+    return plan_prompt(pl, b, T, H, K, S_max, d, sms) ? pl.bytes : 0;
+  });
 }
 
 int gqa_prompt_scores(float* scores, const void* q, const void* k_cache, const int32_t* seqlens, int B, int T, int H,
@@ -637,8 +657,10 @@ int gqa_prompt_scores(float* scores, const void* q, const void* k_cache, const i
 }
 
 size_t gqa_decode_mxfp4_workspace_bytes(int B, int H, int K, int S_max, int d, int num_splits) {
-  MxPlan pl;
-  return plan_mx(pl, B, H, K, S_max, d, num_splits, sm_count(current_device())) ? pl.bytes : 0;
+  return most_over_batches(B, [&](int b, int sms) {
+    MxPlan pl;
+    return plan_mx(pl, b, H, K, S_max, d, num_splits, sms) ? pl.bytes : 0;
+  });
 }
 
 int gqa_decode_mxfp4(void* out, const void* q, const uint8_t* k_codes, const uint8_t* k_scales,
