@@ -157,8 +157,8 @@ __device__ __forceinline__ float load_q_frag_mx(uint32_t (&qf)[kMxD / 16][2], co
   }
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // 2^8 / 2^floor(log2 top): exponent fields 27 .. 253 keep both powers in range
-  const uint32_t e = min(max(top >> 23, 27u), 246u);
+  // 2^8 / 2^floor(log2 top): exponent fields 27 .. 253 keep both powers in range (an element of 254 is below 2^10 then)
+  const uint32_t e = min(max(top >> 23, 27u), 253u);
   const float down = __uint_as_float((262u - e) << 23), up = __uint_as_float((e - 8u) << 23);
 #pragma unroll
   for (int b = 0; b < 4; ++b)
