@@ -19,16 +19,21 @@
 //     turns into a register of the A operand. P^T takes the same key order.
 //
 // P 2^(E_v - 127) leaves fp16's range, so each warp holds a reference exponent
-// R per block and multiplies 2^10 P by 2^(E_v - R + 1). While every E_v of the
-// step lies in [R - 15, R] (E_v = R - j costs j bits of the range) that product
-// holds P's 11 bits down to P = 2^(j - 25) and anything of it down to
-// 2^(j - 35). A step outside the range raises R, or when the range itself is
-// too small takes the same product in bf16, whose exponents need no reference
-// (slower: a further conversion per code).
+// R per block and multiplies 2^13 P by 2^(E_v - R + 1). At E_v = R - j that
+// product holds P's 11 bits down to P = 2^(j - 28) and multiples of 2^(j - 38)
+// below. It is taken while every E_v of the step lies in [R - 11, R], so that a
+// weight is off by 2^-12 of itself or 2^-28 of the largest at most: the
+// rounding of half a million equal weights stays below bf16's. (With 2^10 P and
+// j up to 15, 60000 weights of 1.06 2^-17 beside one of 1 were off by 6 %
+// each.) A step outside the range raises R, or, where its own scales lie
+// further apart, takes the same product in bf16 (2^-9 of each weight; slower: a
+// further conversion per code).
 //
 // P is relative to a reference score m that follows the running maximum only
-// when a step exceeds it by 2^4: the exchange between lanes that finds the
-// maximum is then a rare step, and P stays below 2^14.
+// when a step exceeds it by 2^1: the exchange between lanes that finds the
+// maximum is then a rare step, and P stays at 2 or below. A lag of 2^4 would
+// cost three bits of P for 1 to 2 % of the time (the batches below: 27.1 and
+// 73.0 us against 27.4 and 74.5 at the same time).
 //
 // Bound: the consumers. 136 bytes a key would stream at 5.6 TB/s through this
 // ring (47 us for 32 sequences of 1K to 16K tokens, 64 query and 8 KV heads);
@@ -50,9 +55,9 @@ constexpr int kMxWarpKeys = 32;
 constexpr int kMxTileKeys = kMxWarps * kMxWarpKeys;
 constexpr int kMxStages = 3;
 constexpr int kMxCtasPerSm = 3;
-constexpr float kMxLag = 4.f;    // how far scores may pass m
-constexpr float kMxBias = 10.f;  // 2^(x - m + kMxBias + 1) stays below fp16's 65504
-constexpr int kMxSpan = 15;      // E_v of the fp16 product: [R - kMxSpan, R]
+constexpr float kMxLag = 1.f;    // how far scores may pass m
+constexpr float kMxBias = 13.f;  // 2^(x - m + kMxBias + 1) stays below fp16's 65504
+constexpr int kMxSpan = 11;      // E_v of the fp16 product: [R - kMxSpan, R]
 constexpr int kMxHeadroom = 2;   // a raised R lies this far above the step's largest E_v
 
 struct MxCfg {
@@ -170,7 +175,7 @@ __device__ __forceinline__ float load_q_frag_mx(uint32_t (&qf)[kMxD / 16][2], co
   return up;
 }
 
-// The step's V scales do not lie within every block's [R - 15, R] (in some
+// The step's V scales do not lie within every block's [R - kMxSpan, R] (in some
 // lane): raise the references that have to be. True if all lie within then.
 __device__ __forceinline__ bool mx_rebase(MxState& st, uint32_t own, bool valid) {
   uint32_t ref = 0;
@@ -293,10 +298,13 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
   for (int i = 0; i < 4; ++i) ev[i] = *reinterpret_cast<const uint2*>(sv + kb + 2 * (lane & 3) + 8 * i);
   const uint32_t own = sv[kb + lane];
   const bool own_valid = kb + lane < rows;
-  // R - E of each byte in 0 .. 15: the bytes in two halves with a guard bit above each
+  // R - E of each byte in 0 .. kMxSpan: it and itself + 15 - kMxSpan in 0 .. 15, the bytes in two halves with a guard
+  // bit above each
+  constexpr uint32_t kMore = (15u - kMxSpan) * 0x10001u;
   const uint32_t d0 = ((st.ref & 0x00ff00ffu) | 0x01000100u) - (own & 0x00ff00ffu);
   const uint32_t d1 = (((st.ref >> 8) & 0x00ff00ffu) | 0x01000100u) - ((own >> 8) & 0x00ff00ffu);
-  const bool fits = (((d0 & 0x01f001f0u) ^ 0x01000100u) | ((d1 & 0x01f001f0u) ^ 0x01000100u)) == 0u;
+  const bool fits = ((((d0 ^ 0x01000100u) | ((d0 + kMore) ^ 0x01000100u)) |
+                      ((d1 ^ 0x01000100u) | ((d1 + kMore) ^ 0x01000100u))) & 0x01f001f0u) == 0u;
   bool fast = __all_sync(0xffffffffu, fits || !own_valid);
   if (!fast) fast = mx_rebase(st, own, own_valid);
   const uint32_t ref = st.ref;

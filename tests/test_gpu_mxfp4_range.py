@@ -36,3 +36,25 @@ def test_decode_queries_near_the_end_of_bfloat16(gqa, top):
     q = host(torch.from_numpy(q).float().bfloat16())
     assert np.isfinite(oracle.widen(q)).all()
     check_decode(gqa, q, cache, (S,), 0.3, what=f"{top}")
+
+
+def sink_and_tail(S, far, seed):
+    """Key 0 scores 4, key 1 -6, the others 0 (q = 1 in dim 0). V rows of one block scale, but that of key 1, 2^far above."""
+    k, v = np.zeros((S, D), np.float32), np.abs(synth.normal((S, D), synth.F32, seed, 1)).clip(0, 2.9).astype(np.float32)
+    v[:, ::32] = 3.0
+    k[0, 0], k[1, 0] = 4.0, -6.0
+    v[1] *= 2.0 ** far
+    cache = [a.reshape(1, 1, S, -1) for x in (k, v) for a in cache_ops.mxfp4_quantize(x)]
+    q = np.zeros((1, 8, D), np.float32)
+    q[..., 0] = 1.0
+    return cache, host(torch.from_numpy(q).bfloat16())
+
+
+@pytest.mark.parametrize("far", [0, 8, 9, 10, 11, 12, 13, 14, 40, 90])
+@pytest.mark.parametrize("weight", [1.06, 1.19, 1.94])
+def test_decode_a_flat_tail_beside_one_large_block(gqa, far, weight):
+    # 60000 keys of weight 2^-17 make up half of the result, and what the rounding takes off one of them it takes off
+    # all; key 1 weighs 2^-40. 2^-8: bfloat16 weights, for scales that do not fit one fp16 range
+    cache, q = sink_and_tail(60000, far, 0x3902)
+    check_decode(gqa, q, cache, (60000,), (17 - np.log2(weight)) * np.log(2.0) / 4.0, splits=1, p_step=2.0 ** -8,
+                 what=f"{far} {weight}")
