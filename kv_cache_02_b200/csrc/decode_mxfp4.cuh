@@ -27,7 +27,9 @@
 // j up to 15, 60000 weights of 1.06 2^-17 beside one of 1 were off by 6 %
 // each.) A step outside the range raises R, or, where its own scales lie
 // further apart, takes the same product in bf16 (2^-9 of each weight; slower: a
-// further conversion per code).
+// further conversion per code). There R need not reach E_v, only the largest P
+// 2^(E_v - 127): a value of a huge scale and no weight leaves the others theirs.
+// What lies 2^126 below the largest product of a block counts as zero.
 //
 // P is relative to a reference score m that follows the running maximum only
 // when a step exceeds it by 2^1: the exchange between lanes that finds the
@@ -175,42 +177,74 @@ __device__ __forceinline__ float load_q_frag_mx(uint32_t (&qf)[kMxD / 16][2], co
   return up;
 }
 
+// The references to `ref`, each at or above what it was
+__device__ __forceinline__ void mx_raise(MxState& st, uint32_t ref) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t up = ((ref >> (8 * b)) & 255u) - ((st.ref >> (8 * b)) & 255u);
+    const float f = up > 126u ? 0.f : __uint_as_float((127u - up) << 23);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) st.o[2 * b + i][j] *= f;
+  }
+  st.ref = ref;
+}
+
 // The step's V scales do not lie within every block's [R - kMxSpan, R] (in some
-// lane): raise the references that have to be. True if all lie within then.
+// lane). Where each block's are close enough to one another for the fp16
+// product, raise the references that have to be. True if all lie within then.
 __device__ __forceinline__ bool mx_rebase(MxState& st, uint32_t own, bool valid) {
   uint32_t ref = 0;
   bool fits = true;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const uint32_t e = (own >> (8 * b)) & 255u;
-    const uint32_t top = __reduce_max_sync(0xffffffffu, valid && e != 255u ? e : 0u);
-    const uint32_t old = (st.ref >> (8 * b)) & 255u;
-    uint32_t r = old;
-    if (top > old) {
-      r = min(254u, top + kMxHeadroom);
-      const float f = r - old > 126u ? 0.f : __uint_as_float((127u - (r - old)) << 23);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) st.o[2 * b + i][j] *= f;
-    }
-    fits = fits && (!valid || (e <= r && r - e <= (uint32_t)kMxSpan));
+    const uint32_t top = __reduce_max_sync(0xffffffffu, valid ? e : 0u);
+    const uint32_t low = __reduce_min_sync(0xffffffffu, valid ? e : 255u);
+    const uint32_t r = max((st.ref >> (8 * b)) & 255u, min(min(top + kMxHeadroom, low + kMxSpan), 254u));
+    fits = fits && top <= r && r <= low + kMxSpan;  // a NaN's 255 does not
     ref |= r << (8 * b);
   }
-  st.ref = ref;
-  return __all_sync(0xffffffffu, fits);
+  if (fits) mx_raise(st, ref);
+  return fits;
 }
 
-// 2^(E - R + 1) as bf16 bits; E <= R or 255 (NaN)
+// For the bfloat16 product: R at floor(log2 P) + E_v of every key and head or above, so that no product overflows, and
+// no higher, so that values of a large scale and no weight do not push the others out of float32's range.
+__device__ __forceinline__ void mx_follow(MxState& st, const float (&pa)[4], const float (&pb)[4], const uint32_t* sv,
+                                          int key0, int rows, int head, int nh) {
+  int need[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float p = fmaxf(head < nh ? pa[i] : 0.f, head + 1 < nh ? pb[i] : 0.f);
+    const int lg = (int)(__float_as_uint(p) >> 23) - 127 - (int)kMxBias;
+    if (key0 + 8 * i >= rows || lg < -126) continue;
+    const uint32_t e = sv[key0 + 8 * i];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int eb = (int)((e >> (8 * b)) & 255u);
+      if (eb != 255) need[b] = max(need[b], eb + lg);
+    }
+  }
+  uint32_t ref = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    ref |= max((st.ref >> (8 * b)) & 255u, min((uint32_t)__reduce_max_sync(0xffffffffu, need[b]), 254u)) << (8 * b);
+  mx_raise(st, ref);
+}
+
+// 2^(E - R + 1) as bf16 bits (NaN for E = 255). Beyond 2^127 P is below 2^-126 of the largest: 0, as below 2^-126.
 __device__ __forceinline__ uint32_t mx_bf16_scale(uint32_t e, uint32_t r) {
-  return e == 255u ? 0x7fc0u : r - e > 126u ? 0u : (128u - (r - e)) << 7;
+  const uint32_t f = e + 128u - r;  // exponent field
+  return e == 255u ? 0x7fc0u : f - 1u < 254u ? f << 7 : 0u;
 }
 
 // One warp's 32 keys (kb .. kb + 31) of the tile in `stage`; `rows` keys of
-// the tile are valid, kb < rows. f_a, f_b: scale * log2(e) * the power of two
-// of the lane's heads.
+// the tile are valid, kb < rows; nh heads. f_a, f_b: scale * log2(e) * the power
+// of two of the lane's heads.
 __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[kMxD / 16][2], float f_a, float f_b,
-                                             const uint8_t* stage, int kb, int rows, int lane) {
+                                             const uint8_t* stage, int kb, int rows, int lane, int nh) {
   using C = MxCfg;
   const uint32_t k_base = smem_u32(stage);
   const uint32_t v_base = k_base + C::kCodeBytes;
@@ -306,7 +340,10 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
   const bool fits = ((((d0 ^ 0x01000100u) | ((d0 + kMore) ^ 0x01000100u)) |
                       ((d1 ^ 0x01000100u) | ((d1 + kMore) ^ 0x01000100u))) & 0x01f001f0u) == 0u;
   bool fast = __all_sync(0xffffffffu, fits || !own_valid);
-  if (!fast) fast = mx_rebase(st, own, own_valid);
+  if (!fast) {
+    fast = mx_rebase(st, own, own_valid);
+    if (!fast) mx_follow(st, pa, pb, sv, key0, rows, 2 * (lane & 3), nh);
+  }
   const uint32_t ref = st.ref;
   if (partial) {
 #pragma unroll
@@ -582,7 +619,7 @@ __global__ void __launch_bounds__(kMxDecThreads, kMxCtasPerSm)
       f_b = __shfl_sync(0xffffffffu, up, 8 * (lane & 3) + 4);
       st.reset();
     }
-    if (kb < si.rows) warp_tile_mx(st, qf, f_a, f_b, stage, kb, si.rows, lane);
+    if (kb < si.rows) warp_tile_mx(st, qf, f_a, f_b, stage, kb, si.rows, lane, cur.nh);
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[s]);
     if (si.flags & kTileLast) mx_epilogue(p, cur, st, merge, (si.flags & kUnitSingleSplit) != 0, tid, warp, lane);

@@ -58,3 +58,38 @@ def test_decode_a_flat_tail_beside_one_large_block(gqa, far, weight):
     cache, q = sink_and_tail(60000, far, 0x3902)
     check_decode(gqa, q, cache, (60000,), (17 - np.log2(weight)) * np.log(2.0) / 4.0, splits=1, p_step=2.0 ** -8,
                  what=f"{far} {weight}")
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("where", [0, 37, 699])
+@pytest.mark.parametrize("scale_v,lower", [(254, 400.0), (254, 80.0), (240, 60.0), (180, 45.0), (254, 87.5), (150, 12.0)])
+def test_decode_a_huge_value_of_no_weight(gqa, scale_v, lower, where, splits):
+    # one key's V block lies up to 2^127 above the others', and its weight as far below: what counts is their product,
+    # and the other keys' values keep theirs. Half of the heads give it next to no weight at all
+    B, H, K, S = 1, 8, 1, 700
+    cache = quantised(B, K, S, 0x3903, spread=0.0)
+    k = oracle.widen(synth.normal((B, K, S, D), synth.BF16, 0x3904, 1)).astype(np.float32)
+    k[..., 0] = 0.0
+    k[0, 0, where, 0] = -4.0
+    cache[0], cache[1] = cache_ops.mxfp4_quantize(k)
+    cache[3] = cache[3].copy()
+    cache[3][0, 0, where, [1, 3]] = scale_v
+    q = oracle.widen(synth.normal((B, H, D), synth.BF16, 0x3904, 2)) * 0.25
+    q[..., 0] = lower / 4.0
+    q[:, ::2, 0] = 100.0
+    q = host(torch.from_numpy(q).float().bfloat16())
+    check_decode(gqa, q, cache, (S,), 1.0, splits, 2.0 ** -8, f"{scale_v} {lower} {where}")
+
+
+def test_decode_values_of_every_size(gqa):
+    # blocks from 2^-127 to 2^127 in no order, weights from 1 down to 2^-120: in bfloat16 every product counts
+    B, H, K, S = 2, 8, 2, 600
+    cache = quantised(B, K, S, 0x3905, spread=0.0)
+    rnd = synth.normal((B, K, S, 4), synth.F64, 0x3906, 1)
+    k = np.zeros((B, K, S, D), np.float32)
+    k[..., 0] = synth.normal((B, K, S), synth.F32, 0x3906, 2)
+    cache[0], cache[1] = cache_ops.mxfp4_quantize(k)
+    cache[3] = np.clip(127 + 45 * rnd, 0, 240).astype(np.uint8)
+    q = np.zeros((B, H, D), np.float32)
+    q[..., 0] = np.linspace(1.0, 12.0, H)
+    check_decode(gqa, host(torch.from_numpy(q).bfloat16()), cache, (S, S - 5), 1.0, 1, 2.0 ** -8, "every size")
