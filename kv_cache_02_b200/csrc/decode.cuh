@@ -1270,6 +1270,8 @@ __global__ void __launch_bounds__(NT) decode_combine_kernel(OutT* __restrict__ o
   M = sred[0];
 #pragma unroll
   for (int q = 1; q < NW; ++q) M = fmaxf(M, sred[q]);
+  // no split has a maximum: what their sums hold (0 from gqa_decode_mxfp4, NaN otherwise) against any finite one
+  if (M == -INFINITY) M = 0.f;
   // weights 2^(m_s - M) and L = sum l_s 2^(m_s - M)
   float L = 0.f;
   if (tid < ns) {
@@ -1321,7 +1323,7 @@ __global__ void __launch_bounds__(NT) decode_combine_kernel(OutT* __restrict__ o
     float Lt = 0.f;
 #pragma unroll
     for (int q = 0; q < NW; ++q) Lt += sred[NW + q];
-    const float inv = 1.f / Lt;
+    const float inv = Lt == 0.f ? 0.f : 1.f / Lt;  // no weight: zeros, as without keys
     float4 t = sacc[0][tid];
 #pragma unroll 8
     for (int q = 1; q < R; ++q) {

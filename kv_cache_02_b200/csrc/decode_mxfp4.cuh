@@ -303,7 +303,9 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
       mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
     }
     const float mn_a = fmaxf(st.m_a, mx_a), mn_b = fmaxf(st.m_b, mx_b);
-    const float al_a = fast_exp2(st.m_a - mn_a), al_b = fast_exp2(st.m_b - mn_b);
+    // scores below float32's range alone so far: they weigh nothing, against any finite reference
+    const float al_a = fast_exp2(st.m_a - (mn_a == -INFINITY ? 0.f : mn_a));
+    const float al_b = fast_exp2(st.m_b - (mn_b == -INFINITY ? 0.f : mn_b));
     st.m_a = mn_a;
     st.m_b = mn_b;
     st.l_a *= al_a;
@@ -317,7 +319,7 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
     }
   }
   float pa[4], pb[4];
-  const float r_a = st.m_a - kMxBias, r_b = st.m_b - kMxBias;
+  const float r_a = (st.m_a == -INFINITY ? 0.f : st.m_a) - kMxBias, r_b = (st.m_b == -INFINITY ? 0.f : st.m_b) - kMxBias;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     pa[i] = fast_exp2(xa[i] - r_a);
@@ -463,11 +465,12 @@ __device__ __forceinline__ void mx_epilogue(const DecodeParams& p, const ItemCoo
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kMxWarps; ++w) M = fmaxf(M, red_m[w * 8 + h]);
+    const float ref = M == -INFINITY ? 0.f : M;  // every score of the item below float32's range, or NaN: 0, or NaN
     float L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kMxWarps; ++w) {
-      const float f = fast_exp2(red_m[w * 8 + h] - M);
+      const float f = fast_exp2(red_m[w * 8 + h] - ref);
       const float4 v = *reinterpret_cast<const float4*>(red_o + (w * kDecHeadsPerCta + h) * D + dim);
       L = fmaf(red_l[w * 8 + h], f, L);
       O.x = fmaf(v.x, f, O.x);
@@ -476,6 +479,7 @@ __device__ __forceinline__ void mx_epilogue(const DecodeParams& p, const ItemCoo
       O.w = fmaf(v.w, f, O.w);
     }
     if (single) {
+      if (L == 0.f) L = 1.f;  // no weight: zeros, as without keys
       *reinterpret_cast<uint2*>(out_row + h * D + dim) =
           make_uint2(pack_bf16x2(O.x / L, O.y / L), pack_bf16x2(O.z / L, O.w / L));
     } else {

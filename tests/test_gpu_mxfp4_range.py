@@ -93,3 +93,34 @@ def test_decode_values_of_every_size(gqa):
     q = np.zeros((B, H, D), np.float32)
     q[..., 0] = np.linspace(1.0, 12.0, H)
     check_decode(gqa, host(torch.from_numpy(q).bfloat16()), cache, (S, S - 5), 1.0, 1, 2.0 ** -8, "every size")
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2, 7])
+def test_decode_scores_below_float32(gqa, splits):
+    # keys of scale 2^127 against q: scores of -2^130 and beyond. They weigh nothing: the first 128 and a few others of
+    # head group 0, all of group 1 (zeros, whether one split holds them or several)
+    B, H, K, S = 2, 6, 2, 1400
+    cache = quantised(B, K, S, 0x3907, spread=0.0)
+    k = oracle.widen(synth.normal((B, K, S, D), synth.BF16, 0x3908, 1)).astype(np.float32)
+    k[..., 0] = 0.0
+    masked = np.zeros((B, K, S), bool)
+    masked[:, 0, [*range(130), 700, 1390]] = True
+    masked[:, 1] = True
+    k[masked] = 0.0
+    k[masked, 0] = -6.0
+    cache[0], cache[1] = cache_ops.mxfp4_quantize(k)
+    cache[1] = np.where(masked[..., None] & (np.arange(4) == 0), 254, cache[1]).astype(np.uint8)
+    q = oracle.widen(synth.normal((B, H, D), synth.BF16, 0x3908, 2))
+    q[..., 0] = 4.0
+    q = host(torch.from_numpy(q).float().bfloat16())
+    out = torch.full((B, H, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(gqa.gqa_decode_mxfp4_workspace_bytes(B, H, K, S, D, splits), dtype=torch.uint8, device="cuda")
+    lens = (S, 129)
+    gqa.gqa_decode_mxfp4(out, dev(q), *(dev(c) for c in cache), dev(np.array(lens, np.int32)), D ** -0.5, splits, ws)
+    assert gqa.gqa_get_last_error() == (0, 0)
+    assert not out[:, 3:].any() and not out[1].any()  # sequence 1 ends before its first other key
+    kv, v = cache_ops.mxfp4_values(cache[0], cache[1]), cache_ops.mxfp4_values(cache[2], cache[3])
+    want, _, spread = cache_ops.decode_scores(q[:1, :3], kv[:1, :1], v[:1, :1], (S,), D ** -0.5)
+    a = np.sqrt((oracle.widen(q) ** 2).sum(-1).max() * (k[~masked].astype(np.float64) ** 2).sum(-1).max()) * D ** -0.5
+    tol = (2.0 ** -8 + 2 * D * 2.0 ** -23 * a + 2.0 ** -20) * spread + 2.0 ** -8 * np.abs(want)
+    assert np.all(np.abs(oracle.widen(host(out))[:1, :3] - want) <= tol)
