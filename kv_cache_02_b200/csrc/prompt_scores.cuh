@@ -30,9 +30,11 @@
 // Bound: issue slots and exponentials. A pair takes one exponential per kernel,
 // 16 per clock and SM in the special-function unit: 1024 clocks for a 128 x 128
 // tile (512 for its MMA). kPsPoly of 16 column pairs go to the FMA pipe instead:
-// 2^y = 2^n 2^f, n = round(y), 2^f on [-1/2, 1/2] a polynomial of degree 5
-// (relative error 9.2e-8, below the unit's 2^-22). It costs 12 issue slots a
-// value against 3, so a few pairs are all that helps: 4 x 4096 tokens of 32
+// 2^y = 2^n 2^f, n = round(y), 2^f on [-1/2, 1/2] a polynomial of degree 5: the
+// one of constant term 1 whose largest relative error is least (a linear
+// program over the interval: 9.2e-8), its coefficients rounded to float32
+// (1.1e-7; 1.7e-7 with float32 steps, below the unit's 2^-22). It costs 12 issue
+// slots a value against 3, so a few pairs are all that helps: 4 x 4096 tokens of 32
 // heads, d 128, took 582 + 644 thousand clocks (kRows + kKeys) at 0 of 16,
 // 552 + 624 at 2, 553 + 645 at 3, 573 + 678 at 4.
 #pragma once
