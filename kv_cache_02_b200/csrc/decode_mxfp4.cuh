@@ -26,10 +26,12 @@
 // rounding of half a million equal weights stays below bf16's. (With 2^10 P and
 // j up to 15, 60000 weights of 1.06 2^-17 beside one of 1 were off by 6 %
 // each.) A step outside the range raises R, or, where its own scales lie
-// further apart, takes the same product in bf16 (2^-9 of each weight; slower: a
-// further conversion per code). There R need not reach E_v, only the largest P
-// 2^(E_v - 127): a value of a huge scale and no weight leaves the others theirs.
-// What lies 2^126 below the largest product of a block counts as zero.
+// further apart, takes the same product in bf16 (2^-9 of each weight; a further
+// conversion per code: 138 us for the 32 sequences below where every step does,
+// 84 with the same random rows and scales within 2^9). There R need not reach
+// every E_v, only the largest P 2^(E_v - 127): a value of a huge scale and no
+// weight leaves the others theirs. What lies 2^126 below the largest product of
+// a block counts as zero.
 //
 // P is relative to a reference score m that follows the running maximum only
 // when a step exceeds it by 2^1: the exchange between lanes that finds the
@@ -61,6 +63,7 @@ constexpr float kMxLag = 1.f;    // how far scores may pass m
 constexpr float kMxBias = 13.f;  // 2^(x - m + kMxBias + 1) stays below fp16's 65504
 constexpr int kMxSpan = 11;      // E_v of the fp16 product: [R - kMxSpan, R]
 constexpr int kMxHeadroom = 2;   // a raised R lies this far above the step's largest E_v
+constexpr int kMxSmall = 8;      // keys of weight 2^-8 or more raise R to their E_v
 
 struct MxCfg {
   static constexpr int kCodeBytes = kMxTileKeys * kMxRowBytes;
@@ -210,8 +213,9 @@ __device__ __forceinline__ bool mx_rebase(MxState& st, uint32_t own, bool valid)
   return fits;
 }
 
-// For the bfloat16 product: R at floor(log2 P) + E_v of every key and head or above, so that no product overflows, and
-// no higher, so that values of a large scale and no weight do not push the others out of float32's range.
+// For the bfloat16 product, where some E_v lies above its R: R at floor(log2 P) + E_v of every key and head or above, so
+// that no product overflows, and at the E_v of keys of weight 2^-kMxSmall or more, so that there is seldom a next time.
+// No higher, so that values of a large scale and no weight do not push the others out of float32's range.
 __device__ __forceinline__ void mx_follow(MxState& st, const float (&pa)[4], const float (&pb)[4], const uint32_t* sv,
                                           int key0, int rows, int head, int nh) {
   int need[4] = {0, 0, 0, 0};
@@ -224,7 +228,7 @@ __device__ __forceinline__ void mx_follow(MxState& st, const float (&pa)[4], con
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const int eb = (int)((e >> (8 * b)) & 255u);
-      if (eb != 255) need[b] = max(need[b], eb + lg);
+      if (eb != 255) need[b] = max(need[b], eb + min(lg + kMxSmall, 0));
     }
   }
   uint32_t ref = 0;
@@ -344,7 +348,8 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
   bool fast = __all_sync(0xffffffffu, fits || !own_valid);
   if (!fast) {
     fast = mx_rebase(st, own, own_valid);
-    if (!fast) mx_follow(st, pa, pb, sv, key0, rows, 2 * (lane & 3), nh);
+    const bool above = own_valid && (d0 & d1 & 0x01000100u) != 0x01000100u;  // some E_v > R, or NaN's 255
+    if (!fast && __any_sync(0xffffffffu, above)) mx_follow(st, pa, pb, sv, key0, rows, 2 * (lane & 3), nh);
   }
   const uint32_t ref = st.ref;
   if (partial) {
