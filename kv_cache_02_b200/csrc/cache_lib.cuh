@@ -175,7 +175,8 @@ int decode_scores_impl(void* out, float* scores, const void* q, const void* k_ca
   if (!plan_scores(sp, B, H, K, S_max, d, num_splits, pc != nullptr, sm_count(current_device()))) return GQA_ERR_SHAPE;
   if (!workspace || workspace_bytes < sp.bytes) return GQA_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return GQA_ERR_ALIGN;
-  // the join: four rows a thread, or eight where those CTAs would not all be resident (four per SM)
+  // the join: four rows a thread, or eight where those CTAs would not all be resident (four per SM; both sides
+  // measured beside scores_finish_kernel)
   const int acc_keys = 4 * gqa::kAccThreads;
   const bool eight = (long long)B * K * ((S_max + acc_keys - 1) / acc_keys) > 4ll * sm_count(current_device());
   const long long chunks = eight ? (S_max + 2 * acc_keys - 1) / (2 * acc_keys) : (S_max + acc_keys - 1) / acc_keys;
@@ -461,9 +462,17 @@ bool plan_mx(MxPlan& pl, int B, int H, int K, int S_max, int d, int num_splits, 
   if (num_splits > 0) {
     splits = std::min(num_splits, max_splits);
   } else {
-    // two items per resident CTA (8 x 32 x 8 x 128 over 8192 keys: 22.7 us at one, 24.3 at two, 25.3 at three;
-    // one leaves nothing to balance unequal lengths with), four for batches of many units, which are seldom of one
-    // length (32 sequences of 1K to 16K tokens: 71.7 us at four, 78.4 at two)
+    // Items per resident CTA: sequences of one length want few, unequal ones many, and the plan does not know the
+    // lengths. 8 KV heads of 4 query heads, 16384 tokens each / 1K to 16K, us at one, two, four and six:
+    //    16 units   15.8  17.8  17.8  17.9 /  14.7  13.1  13.1  13.1
+    //    64         38.0  39.0  43.3  43.5 /  35.0  27.6  30.6  30.8
+    //    96         59.7  58.0  57.4  58.5 /  46.0  39.2  41.6  42.6
+    //   128         73.1  72.7  67.2  73.0 /  54.6  49.9  50.7  50.9
+    //   192         94.6  93.8  98.7  94.4 /  70.7  68.3  62.6  62.5
+    //   256        138.6 117.6 123.9 124.5 /  97.8  85.4  81.2  80.9
+    //   512        260   221   237   227   / 178   148   137   133
+    // Two is the best or near it for both below 128 units; from there on two costs unequal lengths up to 9 % and
+    // four equal ones up to 7 %, and a batch of many sequences is seldom of one length.
     const long long target = (units >= 128 ? 4ll : 2ll) * gqa::kMxCtasPerSm * sms;
     splits = (int)std::max<long long>(1, (target + units - 1) / std::max<long long>(units, 1));
     splits = std::min(splits, std::max(1, (S_max + 511) / 512));

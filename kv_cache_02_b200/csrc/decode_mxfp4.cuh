@@ -41,10 +41,11 @@
 //
 // Bound: the consumers. 136 bytes a key would stream at 5.6 TB/s through this
 // ring (47 us for 32 sequences of 1K to 16K tokens, 64 query and 8 KV heads);
-// with the scores alone it is 54 us, with the weighted sum alone 60, with both
-// 72 (3.6 TB/s): 480 instructions for 32 keys of 8 heads, half of them on the
-// half-rate ALU pipe (codes, nibbles, scales). 8 x 8192 tokens of 32 and 8
-// heads: 25 us. No faster: eight consumer warps a CTA (76 us), a ring of four
+// with both products it is 75 us (3.5 TB/s): 501 instructions for 32 keys of 8
+// heads, half of them on the half-rate ALU pipe (codes, nibbles, scales). At a
+// lag of 2^4 (480 instructions, 72 us) the scores alone took 54 us, the weighted
+// sum alone 60. 8 x 8192 tokens of 32 and 8 heads, with the append before it: 27
+// us. No faster: eight consumer warps a CTA (76 us for 72), a ring of four
 // stages (72 to 74), V codes loaded before the softmax, L2 prefetches.
 #pragma once
 
@@ -77,6 +78,7 @@ struct MxCfg {
   static constexpr int kSmemBytes = kBarOff + 2 * kMxStages * 8;
 };
 static_assert(MxCfg::kStageBytes % 1024 == 0, "stages start on the swizzle pattern");
+static_assert(kMxSpan <= 15, "a half's exponent field holds E - R + 16 in five bits");
 
 struct MxParams {
   const uint8_t *k_scales, *v_scales;
@@ -213,9 +215,11 @@ __device__ __forceinline__ bool mx_rebase(MxState& st, uint32_t own, bool valid)
   return fits;
 }
 
-// For the bfloat16 product, where some E_v lies above its R: R at floor(log2 P) + E_v of every key and head or above, so
-// that no product overflows, and at the E_v of keys of weight 2^-kMxSmall or more, so that there is seldom a next time.
-// No higher, so that values of a large scale and no weight do not push the others out of float32's range.
+// For the bfloat16 product, where some E_v lies above its R: R at floor(log2 P)
+// + E_v of every key and head or above, so that no product overflows, and at the
+// E_v of keys of weight 2^-kMxSmall or more, so that there is seldom a next time.
+// No higher, so that values of a large scale and no weight do not push the
+// others out of float32's range.
 __device__ __forceinline__ void mx_follow(MxState& st, const float (&pa)[4], const float (&pb)[4], const uint32_t* sv,
                                           int key0, int rows, int head, int nh) {
   int need[4] = {0, 0, 0, 0};
@@ -323,7 +327,8 @@ __device__ __forceinline__ void warp_tile_mx(MxState& st, const uint32_t (&qf)[k
     }
   }
   float pa[4], pb[4];
-  const float r_a = (st.m_a == -INFINITY ? 0.f : st.m_a) - kMxBias, r_b = (st.m_b == -INFINITY ? 0.f : st.m_b) - kMxBias;
+  const float r_a = (st.m_a == -INFINITY ? 0.f : st.m_a) - kMxBias;
+  const float r_b = (st.m_b == -INFINITY ? 0.f : st.m_b) - kMxBias;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     pa[i] = fast_exp2(xa[i] - r_a);

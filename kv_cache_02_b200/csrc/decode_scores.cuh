@@ -11,9 +11,12 @@
 // instead would cost 2 d bytes a key; the scores are 8 G bytes a key written
 // and read back, mostly in L2.
 //
-// Measured: 8 x 8192 keys of 32 and 8 heads, d 128: 49 us (gqa_decode: 43; the
-// bytes of K and V at a copy's rate: 41); one sequence of 131072 keys, 64 and 8
-// heads: 98 us (82; 82), the join of 33 MB of scores included.
+// Measured, in a graph: 8 x 8192 keys of 32 and 8 heads, d 128: 52 us
+// (gqa_decode: 47; the bytes at a copy's rate: 42); one sequence of 131072 keys,
+// 64 and 8 heads: 102 us (86; 83), the join of 33 MB of scores included. Larger
+// groups pay for their scores (8 G bytes a key) and for the tile of every head
+// slice: 64 heads over 131072 keys of 4, 2 and 1 KV heads 85, 92 and 121 us
+// (gqa_decode 59, 55 and 20).
 #pragma once
 
 #include "decode.cuh"
@@ -93,8 +96,10 @@ __device__ __forceinline__ void warp_tile_scores(WarpState<D>& st, const uint32_
   // the second costs 1 % (8 x 8192 keys: 51.5 us in a graph for 50.9)
   const uint32_t h0 = pack_bf16x2(p0, p1), h1 = pack_bf16x2(p2, p3);
   const uint32_t pb0 = movmatrix_trans(h0), pb1 = movmatrix_trans(h1);
-  const uint32_t pl0 = movmatrix_trans(pack_bf16x2(p0 - __uint_as_float(h0 << 16), p1 - __uint_as_float(h0 & 0xffff0000u)));
-  const uint32_t pl1 = movmatrix_trans(pack_bf16x2(p2 - __uint_as_float(h1 << 16), p3 - __uint_as_float(h1 & 0xffff0000u)));
+  auto rest = [](uint32_t h, float lo, float hi) {
+    return pack_bf16x2(lo - __uint_as_float(h << 16), hi - __uint_as_float(h & 0xffff0000u));
+  };
+  const uint32_t pl0 = movmatrix_trans(rest(h0, p0, p1)), pl1 = movmatrix_trans(rest(h1, p2, p3));
   uint32_t mask_lo = 0xffffffffu, mask_hi = 0xffffffffu;
   if (kb + 16 > rows) {
     const int lim = rows - kb;
@@ -291,10 +296,15 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 // columns (summed in a fixed order). Latency bounds it: all that does not
 // depend on (m, l) is asked for first, the scores to be added to into L2 (their
 // values in registers would make them spill). Q = 2 where the CTAs of Q = 1
-// would not all be resident (131072 keys of 8 heads: 98 us a call, for 107).
+// would not all be resident, 592 at a time: whole calls in a graph at Q = 1 and
+// 2, by CTAs of Q = 1: 256 31.9 and 34.1 us, 512 50.5 and 52.4, 576 54.9 and
+// 57.0, 608 68.2 and 68.4, 640 64.0 and 63.3, 1024 (131072 keys of 8 heads)
+// 107.7 and 102.2, 2048 213 and 206.
 constexpr int kAccThreads = 256;
 constexpr int kAccHeads = 64;  // heads whose (M, 1 / L) are held at a time
-constexpr int kAccFlight = 4;  // float4 of scores that a thread asks for at once
+// float4 of scores that a thread asks for at once (512 and 1024 CTAs: 50.5 and 102 us; two 50.8 and 100, eight, which
+// spill, 54.2 and 106)
+constexpr int kAccFlight = 4;
 
 template <int D, int Q>
 __global__ void __launch_bounds__(kAccThreads, 4)
