@@ -107,7 +107,7 @@ GQA_API int gqa_qk_norm_rope_paged(void* q_out, void* k_out, void* k_pool, void*
  *          what the caller (or gqa_kv_evict) left there, normally 0. The sum
  *          over a group's heads is taken in a fixed order: results repeat
  *          bit for bit.
- * Sums are float32; a weight meets the values rounded by 2^-18 of itself.
+ * Sums are float32; a weight meets the values rounded by 2^-15 of itself.
  * A key whose score is -inf weighs nothing. A query head that has no other
  * key adds nothing to the scores and its output is zeros, as for an empty
  * sequence. A NaN score makes all of its head's weights and its output NaN.

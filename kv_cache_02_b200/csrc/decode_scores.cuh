@@ -92,13 +92,16 @@ __device__ __forceinline__ void warp_tile_scores(WarpState<D>& st, const uint32_
     st.o[md][3] *= al_b;
   }
 
-  // P as two bfloat16 terms, off by 2^-18 of it: one would be off by 2^-9, as much as the output's own rounding, and
-  // the second costs 1 % (8 x 8192 keys: 51.5 us in a graph for 50.9)
-  const uint32_t h0 = pack_bf16x2(p0, p1), h1 = pack_bf16x2(p2, p3);
-  const uint32_t pb0 = movmatrix_trans(h0), pb1 = movmatrix_trans(h1);
+  // P as two bfloat16 terms, off by 2^-15 of it: one would be off by 2^-9, as much as the output's own rounding, and
+  // the second costs 1 % (8 x 8192 keys: 51.5 us in a graph for 50.9). The first is the value below the one that P
+  // cut off gives, so that the second is above 0 too: neither makes NaN of an infinite value.
+  auto below = [](float p) { return max(__float_as_uint(p), 0x10000u) - 0x10000u; };
+  auto first = [&](float lo, float hi) { return __byte_perm(below(lo), below(hi), 0x7632); };
   auto rest = [](uint32_t h, float lo, float hi) {
     return pack_bf16x2(lo - __uint_as_float(h << 16), hi - __uint_as_float(h & 0xffff0000u));
   };
+  const uint32_t h0 = first(p0, p1), h1 = first(p2, p3);
+  const uint32_t pb0 = movmatrix_trans(h0), pb1 = movmatrix_trans(h1);
   const uint32_t pl0 = movmatrix_trans(rest(h0, p0, p1)), pl1 = movmatrix_trans(rest(h1, p2, p3));
   uint32_t mask_lo = 0xffffffffu, mask_hi = 0xffffffffu;
   if (kb + 16 > rows) {
