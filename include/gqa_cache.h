@@ -231,6 +231,8 @@ GQA_API int gqa_kv_evict_paged(void* k_pool, void* v_pool, const int32_t* block_
  * the values with a rounding of at most 2^-9 of itself or 2^-28 of the largest
  * weight of its split. A key whose score falls below float32's range weighs
  * nothing; a head that has no other key gets zeros, as for an empty sequence.
+ * (K block scales above 2^108 may take a score out of float32's range whatever
+ * q is: a head's elements meet them at 2^8 times their share of its largest.)
  */
 GQA_API int gqa_kv_append_mxfp4(uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales,
                                 const void* k_new, const void* v_new, const int32_t* pos, int B, int T, int K,

@@ -139,7 +139,7 @@ __device__ __forceinline__ uint32_t odd_nibbles(uint32_t a, uint32_t b) {
 // that and over 2^(R - 127) of its 32-dim block; m is the scores' reference.
 struct MxState {
   float m_a, m_b, l_a, l_b;
-  uint32_t ref;  // R of block i in byte i, 16 or more; the same in all lanes
+  uint32_t ref;  // R of block i in byte i, 16 or more (above kMxBias + 1); the same in all lanes
   float o[kMxD / 16][4];
   __device__ __forceinline__ void reset() {
     m_a = m_b = -INFINITY;
@@ -451,15 +451,18 @@ __device__ __forceinline__ void mx_epilogue(const DecodeParams& p, const ItemCoo
     l_b += __shfl_xor_sync(0xffffffffu, l_b, off);
   }
   const int ha = 2 * (lane & 3);
+  constexpr uint32_t kBias = (uint32_t)kMxBias;
   if (lane < 4) {
+    const float f = __uint_as_float((127u - kBias) << 23);
     red_m[warp * 8 + ha] = st.m_a;
     red_m[warp * 8 + ha + 1] = st.m_b;
-    red_l[warp * 8 + ha] = l_a;
-    red_l[warp * 8 + ha + 1] = l_b;
+    red_l[warp * 8 + ha] = l_a * f;
+    red_l[warp * 8 + ha + 1] = l_b * f;
   }
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    const float f = __uint_as_float((((st.ref >> (8 * b)) & 255u) - 1u) << 23);  // 2^(R - 127) / 2
+    // 2^(R - 127) / 2^(kMxBias + 1): large values are not to overflow before the division by l
+    const float f = __uint_as_float((((st.ref >> (8 * b)) & 255u) - 1u - kBias) << 23);
     const int dim = 32 * b + 4 * (lane >> 2);
     const float* o0 = st.o[2 * b];
     const float* o1 = st.o[2 * b + 1];

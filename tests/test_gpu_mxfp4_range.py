@@ -124,3 +124,21 @@ def test_decode_scores_below_float32(gqa, splits):
     a = np.sqrt((oracle.widen(q) ** 2).sum(-1).max() * (k[~masked].astype(np.float64) ** 2).sum(-1).max()) * D ** -0.5
     tol = (2.0 ** -8 + 2 * D * 2.0 ** -23 * a + 2.0 ** -20) * spread + 2.0 ** -8 * np.abs(want)
     assert np.all(np.abs(oracle.widen(host(out))[:1, :3] - want) <= tol)
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("scale_v", [235, 243, 248, 252, 253])
+def test_decode_values_near_the_end_of_float32(gqa, scale_v, splits):
+    # few keys, so that sum p v stays in range: 2^126 of weight 1, smaller ones beside it
+    B, H, K, S = 1, 8, 2, 260
+    cache = quantised(B, K, S, 0x3909, spread=0.0)
+    k = np.zeros((B, K, S, D), np.float32)
+    k[:, :, [3, 200], 0] = 6.0, 5.0
+    cache[0], cache[1] = cache_ops.mxfp4_quantize(k)
+    cache[3] = np.full_like(cache[3], 127)
+    cache[3][:, :, 3] = scale_v
+    cache[2][:, :, 3] = 0x1A  # -1, 0.5
+    cache[3][:, :, 200, 2] = scale_v - 9
+    q = np.zeros((B, H, D), np.float32)
+    q[..., 0] = np.linspace(2.0, 16.0, H)
+    check_decode(gqa, host(torch.from_numpy(q).bfloat16()), cache, (S,), 1.0, splits, 2.0 ** -8, f"{scale_v}")
